@@ -328,6 +328,163 @@ int moe_fp4_prenorm_bf16(const float *x, uint16_t *u, int32_t T, int32_t H, floa
 int moe_fp4_quant_mxfp8(const uint16_t *src, int32_t rows, int32_t K, uint8_t *codes,
                         uint8_t *scales, hipStream_t stream);
 
+/* ======================================================================
+ * Operators around the routed experts: 16-bit products grouped by expert, the
+ * dense product with its epilogue, and norms with weights, each with its
+ * backward pass.  They follow the conventions above (device pointers, stream,
+ * host validation before any HIP call, no allocation, no state), with these
+ * additions:
+ *   - A row stride (ld*) counts elements; 0 means dense rows.  Otherwise it is
+ *     at least the row's width (EINVAL).
+ *   - Arrays need the alignment of their elements only (EALIGN).  Rows that
+ *     start on 16-byte boundaries take the faster kernels.
+ *   - Zero rows (P, M or T = 0) are allowed; arrays of no elements may be NULL.
+ *   - Sums are fp32 in a fixed order: the same inputs give the same bits.  Each
+ *     result is rounded once, to nearest, ties to even.
+ *   - A workspace is sized by the operator's *_workspace_size, 256-byte
+ *     aligned, needs no initialisation and may be NULL when its size is 0.  It
+ *     belongs to one call at a time; two captured graphs that may replay at
+ *     once need two.
+ *   - An output must not overlap an input unless the operator says so.
+ * ====================================================================== */
+
+/* ---- element types */
+#define MOE_FP4_F32   0
+#define MOE_FP4_BF16  1
+#define MOE_FP4_F16   2
+
+/* ---- products grouped by expert (rows in expert order, ragged)
+ *   forward  y[s][n]     = sum_c x[src(s)][c] * w[e(s)][n][c]
+ *   dgrad    dx[s][c]    = sum_n dy[s][n] * w[e(s)][n][c]
+ *   wgrad    dw[e][n][c] = sum over e's rows s of dy[s][n] * x[src(s)][c]
+ * Expert e owns rows offsets[e] .. offsets[e+1]-1 of y, dy and dx, as
+ * moe_fp4_route writes them.  With `rows` (int32 [P], e.g. moe_fp4_route's
+ * sorted_pairs), src(s) = rows[s] / row_div: with row_div = k, pair p = t * k + j
+ * reads token t.  Without it src(s) = s.  offsets and rows are device data the
+ * host does not see: an entry of rows outside [0, R * row_div) reads as a row
+ * of zeros, offsets are held to [0, P]; offsets that are not ascending give
+ * rows without a defined value, never an access outside the arrays.  Rows of
+ * y and dx outside [offsets[0], offsets[E]) are left as they were.  An expert
+ * without rows gets dw = 0 (unchanged with MOE_FP4_ACCUMULATE). */
+typedef struct {
+  int32_t E;          /* experts: 1 .. 1024                                     */
+  int32_t P;          /* rows in expert order: 0 .. 1048576                     */
+  int32_t N;          /* outputs of an expert (rows of its weight): 1 .. 65536  */
+  int32_t K;          /* inputs of an expert (columns of its weight): 1 .. 65536 */
+  int32_t R;          /* rows of x: 0 .. 1048576 (used with `rows` only)        */
+  int32_t row_div;    /* >= 1 (used with `rows` only)                           */
+  int32_t type;       /* x, w and dy: MOE_FP4_BF16 or MOE_FP4_F16               */
+  int32_t out_type;   /* the result: `type` or MOE_FP4_F32                      */
+  int64_t ldx;        /* x [P or R][K] and dx [P][K]                            */
+  int64_t ldw;        /* w and dw [E][N][K]                                     */
+  int64_t ldy;        /* y and dy [P][N]                                        */
+  int64_t expert_stride; /* elements between experts' weights, 0: N * ldw; at   */
+                         /* least (N - 1) * ldw + K                             */
+} moe_fp4_grouped_dims;
+
+#define MOE_FP4_GROUPED_FORWARD 0
+#define MOE_FP4_GROUPED_DGRAD   1
+#define MOE_FP4_GROUPED_WGRAD   2
+
+/* Bytes of workspace the call `op` (MOE_FP4_GROUPED_*) needs.  Errors: EINVAL, EUNSUPPORTED. */
+int moe_fp4_grouped_workspace_size(const moe_fp4_grouped_dims *dims, int op, size_t *bytes);
+
+/* flags: MOE_FP4_ACCUMULATE adds to the result (in fp32, rounded once).
+ * Errors: EINVAL, EUNSUPPORTED (sizes, types, flags), EALIGN, EWORKSPACE, EHIP. */
+int moe_fp4_grouped_forward(const moe_fp4_grouped_dims *dims, const void *x, const void *w,
+                            const int32_t *offsets, const int32_t *rows, void *y, int flags,
+                            void *ws, size_t ws_bytes, hipStream_t stream);
+int moe_fp4_grouped_dgrad(const moe_fp4_grouped_dims *dims, const void *dy, const void *w,
+                          const int32_t *offsets, void *dx, int flags, void *ws, size_t ws_bytes,
+                          hipStream_t stream);
+int moe_fp4_grouped_wgrad(const moe_fp4_grouped_dims *dims, const void *dy, const void *x,
+                          const int32_t *offsets, const int32_t *rows, void *dw, int flags,
+                          void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- dense product with bias, activation and residual in its epilogue
+ *   z[m][n] = sum_c x[m][c] * w[n][c] + bias[n]
+ *   y[m][n] = act(z[m][n]) + residual[m][n]      (all in fp32, one rounding)
+ * bias, residual and z may be NULL.  z, where given, receives z rounded to
+ * `type`, for the backward pass; act itself takes the unrounded z.  y may be
+ * the residual (same stride). */
+#define MOE_FP4_ACT_NONE      0
+#define MOE_FP4_ACT_RELU      1
+#define MOE_FP4_ACT_GELU      2  /* z * Phi(z)                                          */
+#define MOE_FP4_ACT_GELU_TANH 3  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))     */
+#define MOE_FP4_ACT_SILU      4  /* z * sigmoid(z)                                      */
+
+typedef struct {
+  int32_t M;          /* rows: 0 .. 1048576                                    */
+  int32_t N, K;       /* outputs and inputs: 1 .. 65536                        */
+  int32_t type;       /* x, w, z and dx: MOE_FP4_BF16 or MOE_FP4_F16           */
+  int32_t out_type;   /* y, residual and dy: `type` or MOE_FP4_F32             */
+  int32_t bias_type;  /* bias: any of the three                                */
+  int32_t dw_type;    /* dw: `type` or MOE_FP4_F32 (backward only)             */
+  int32_t act;        /* MOE_FP4_ACT_*                                         */
+  int64_t ldx, ldw, ldy, ldr, ldz; /* x [M][K], w [N][K], y and dy [M][N], residual, z */
+  int64_t lddx, lddw; /* dx [M][K], dw [N][K] (backward only)                  */
+} moe_fp4_linear_dims;
+
+/* Bytes of workspace of moe_fp4_linear (backward = 0) or moe_fp4_linear_backward
+ * (backward = 1).  Errors: EINVAL, EUNSUPPORTED. */
+int moe_fp4_linear_workspace_size(const moe_fp4_linear_dims *dims, int backward, size_t *bytes);
+
+/* flags: MOE_FP4_ACCUMULATE adds to y.
+ * Errors: EINVAL, EUNSUPPORTED (sizes, types, act, flags), EALIGN, EWORKSPACE, EHIP. */
+int moe_fp4_linear(const moe_fp4_linear_dims *dims, const void *x, const void *w, const void *bias,
+                   const void *residual, void *y, void *z, int flags, void *ws, size_t ws_bytes,
+                   hipStream_t stream);
+
+/* The gradients, with dz = dy * act'(z):
+ *   dx = dz W (type)      dw = dz^T x (dw_type)      db[n] = sum_m dz[m][n] (fp32)
+ * Each of dx, dw, db may be NULL (at least one is not).  x is read for dw, w
+ * for dx, z where act is not NONE; they may be NULL otherwise.  dz is rounded
+ * to `type` for the two products (not for db).  The residual's gradient is dy.
+ * flags: MOE_FP4_ACCUMULATE adds to dw and db (dx is always overwritten).
+ * Errors: as moe_fp4_linear. */
+int moe_fp4_linear_backward(const moe_fp4_linear_dims *dims, const void *dy, const void *x,
+                            const void *w, const void *z, void *dx, void *dw, float *db, int flags,
+                            void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* ---- norms with weights
+ *   mean = sum_h x / H (RMS: 0), rstd = 1 / sqrt(sum_h (x - mean)^2 / H + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ * gamma and beta may be NULL (1 and 0).  mean and rstd (fp32 [T]) are written
+ * where not NULL; the backward pass reads them.  y may be x where both have
+ * the same type and stride. */
+#define MOE_FP4_NORM_LAYER 0
+#define MOE_FP4_NORM_RMS   1
+
+typedef struct {
+  int32_t T;          /* rows: 0 .. 1048576                                   */
+  int32_t H;          /* 1 .. 16384                                           */
+  int32_t x_type;     /* x and dx: any of the three                           */
+  int32_t y_type;     /* y and dy: x_type, or any where x_type is MOE_FP4_F32  */
+  int32_t w_type;     /* gamma and beta: any of the three                     */
+  int32_t kind;       /* MOE_FP4_NORM_*                                       */
+  float eps;          /* >= 0                                                 */
+  int64_t ldx, ldy, lddx; /* x, y and dy, dx                                  */
+} moe_fp4_norm_dims;
+
+/* Errors: EINVAL, EUNSUPPORTED (sizes, types, kind), EALIGN, EHIP. */
+int moe_fp4_norm(const moe_fp4_norm_dims *dims, const void *x, const void *gamma, const void *beta,
+                 void *y, float *mean, float *rstd, hipStream_t stream);
+
+int moe_fp4_norm_backward_workspace_size(const moe_fp4_norm_dims *dims, size_t *bytes);
+
+/* With xhat = (x - mean) * rstd and g = dy * gamma:
+ *   dx = rstd * (g - mean_h(g) [layer kind] - xhat * mean_h(g * xhat))
+ *   dgamma = sum_t dy * xhat      dbeta = sum_t dy      (fp32 [H])
+ * Each of dx, dgamma, dbeta may be NULL (at least one is not); mean is not
+ * read for the RMS kind and may be NULL there.  dx may be dy where both have
+ * the same type and stride.  flags: MOE_FP4_ACCUMULATE adds to dgamma and dbeta
+ * (dx is always overwritten).  eps is not read.
+ * Errors: as moe_fp4_norm, and EUNSUPPORTED (flags), EWORKSPACE. */
+int moe_fp4_norm_backward(const moe_fp4_norm_dims *dims, const void *dy, const void *x,
+                          const void *gamma, const float *mean, const float *rstd, void *dx,
+                          float *dgamma, float *dbeta, int flags, void *ws, size_t ws_bytes,
+                          hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *moe_fp4_status_string(int status);
 

@@ -14,3 +14,9 @@ from ._lib import (ACCUMULATE, MODE_AUTO, MODE_DECODE, MODE_PREFILL,  # noqa: F4
                    moe_fp4_forward_residual, moe_fp4_forward_noalloc, moe_fp4_plan, moe_fp4_route_workspace_size,
                    PATH_DECODE_ONE, PATH_DECODE_FEW, PATH_DECODE_MFMA, PATH_PREFILL,
                    PATH_PREFILL_MXFP8, moe_fp4_workspace_size, status_string)
+from ._block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # noqa: F401
+                     GROUPED_DGRAD, GROUPED_FORWARD, GROUPED_WGRAD, NORM_LAYER, NORM_RMS,
+                     moe_fp4_grouped_dgrad, moe_fp4_grouped_forward, moe_fp4_grouped_wgrad,
+                     moe_fp4_grouped_workspace_size, moe_fp4_linear, moe_fp4_linear_backward,
+                     moe_fp4_linear_workspace_size, moe_fp4_norm, moe_fp4_norm_backward,
+                     moe_fp4_norm_backward_workspace_size)

@@ -1,0 +1,84 @@
+// The elementwise part of a dense product's backward pass: dz = dy act'(z) and
+// the bias gradient, its column sums.
+#include "block_device.h"
+
+namespace moe_fp4 {
+namespace {
+
+constexpr int kSlopeCols = 32, kSlopeRows = 8;  // threads of a workgroup
+
+// One pass over dy and z.  Thread (r, c) takes V neighbouring columns of every
+// eighth row of the workgroup's rows and sums them in fp32 before dz is
+// rounded; the eight sums of a column are joined in order and written to
+// part[workgroup row].  dz is rounded to the products' type because it feeds
+// the matrix cores (one rounding, 2^-9 or 2^-12 relative at most); the bias
+// gradient does not see that rounding.
+template <int V>
+__global__ void __launch_bounds__(256) slope_kernel(SlopeArgs g) {
+  __shared__ float s[kSlopeRows][kSlopeCols * V];
+  const int tc = threadIdx.x & (kSlopeCols - 1), tr = threadIdx.x / kSlopeCols;
+  const int j = (blockIdx.x * kSlopeCols + tc) * V;
+  float sum[V] = {};
+  if (j < g.N)
+    for (int64_t i = (int64_t)blockIdx.y * kSlopeRows + tr; i < g.M; i += (int64_t)gridDim.y * kSlopeRows) {
+      float d[V], z[V];
+#pragma unroll
+      for (int r = 0; r < V; ++r) d[r] = load_as_f32(g.dy, i * g.lddy + j + r, g.dy_type);
+      if (g.act != kActNone) {
+#pragma unroll
+        for (int r = 0; r < V; ++r) z[r] = load_as_f32(g.z, i * g.ldz + j + r, g.type);
+#pragma unroll
+        for (int r = 0; r < V; ++r) d[r] *= activate_slope(z[r], g.act);
+      }
+#pragma unroll
+      for (int r = 0; r < V; ++r) {
+        sum[r] += d[r];
+        if (g.dz) store_from_f32(g.dz, i * g.N + j + r, g.type, d[r]);
+      }
+    }
+  if (!g.db) return;
+#pragma unroll
+  for (int r = 0; r < V; ++r) s[tr][tc * V + r] = sum[r];
+  __syncthreads();
+  for (int c = threadIdx.x; c < kSlopeCols * V; c += 256) {
+    const int col = blockIdx.x * kSlopeCols * V + c;
+    if (col >= g.N) break;
+    float v = s[0][c];
+#pragma unroll
+    for (int r = 1; r < kSlopeRows; ++r) v += s[r][c];
+    g.part[(int64_t)blockIdx.y * g.N + col] = v;
+  }
+}
+
+__global__ void __launch_bounds__(256) slope_columns_kernel(const float* part, int parts, int N,
+                                                            float* db, int accumulate) {
+  __shared__ float s[8][32];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), p0 = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < N)
+    for (int p = p0; p < parts; p += 8) v += part[(int64_t)p * N + col];
+  s[p0][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (p0 || col >= N) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += s[i][threadIdx.x & 31];
+  db[col] = accumulate ? db[col] + v : v;
+}
+
+}  // namespace
+
+int slope_blocks(int M) {
+  const int b = (M + 31) / 32;
+  return b < 1 ? 1 : b > 256 ? 256 : b;
+}
+
+hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream) {
+  const dim3 grid((a.N + kSlopeCols - 1) / kSlopeCols, slope_blocks(a.M));
+  hipLaunchKernelGGL(slope_kernel<1>, grid, dim3(256), 0, stream, a);
+  if (a.db)
+    hipLaunchKernelGGL(slope_columns_kernel, dim3((a.N + 31) / 32), dim3(256), 0, stream, a.part,
+                       slope_blocks(a.M), a.N, a.db, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace moe_fp4
