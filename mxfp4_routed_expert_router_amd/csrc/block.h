@@ -48,10 +48,22 @@ struct ProductArgs {
   // [I][J] (wgrad [E][I][J]); 1: none
   int splits;
   float* part;
+  int wide;                // set by launch_product: the epilogue takes four columns at a time
 };
 
 size_t product_workspace(const ProductArgs& a, int op);  // bytes of `part`
 hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream);
+// The products through LDS tiles filled straight from memory, for 16-byte
+// aligned rows whose length is a multiple of 8 (product_lds_takes).
+void launch_product_fwd(const ProductArgs& a, hipStream_t stream);
+void launch_product_dgrad(const ProductArgs& a, hipStream_t stream);
+void launch_product_wgrad(const ProductArgs& a, hipStream_t stream);
+// The most row tiles of BM rows that the experts can have.
+inline int64_t row_tiles_most(const ProductArgs& a, int BM) {
+  if (!a.offsets) return (a.P + BM - 1) / BM;
+  const int64_t live = a.E < a.P ? a.E : a.P;  // experts that can have rows
+  return (a.P + live * (BM - 1)) / BM;
+}
 
 // dz = dy act'(z) in `type`, and the column sums of dz before that rounding.
 struct SlopeArgs {

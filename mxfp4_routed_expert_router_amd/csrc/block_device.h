@@ -102,9 +102,24 @@ __device__ __forceinline__ void segment(const int32_t* offsets, int e, int P, in
   n = hi - lo;
 }
 
-// Row tile `t` of the experts' row tiles laid end to end (ceil(rows / BM) of
-// each): its expert, first row and row count.  False where t is past the last
-// one.  Every wave finds it alone, 64 experts at a time; uniform over the wave.
+// The experts' row tiles laid end to end, ceil(rows / BM) of each: their number.
+// Every wave finds it alone, 64 experts at a time; uniform over the wave.
+__device__ __forceinline__ int row_tiles(const int32_t* offsets, int E, int P, int BM) {
+  if (!offsets) return (P + BM - 1) / BM;
+  const int lane = threadIdx.x & 63;
+  int own = 0;
+  for (int e = lane; e < E; e += 64) {
+    int lo, n;
+    segment(offsets, e, P, lo, n);
+    own += (n + BM - 1) / BM;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) own += __shfl_xor(own, d, 64);
+  return __builtin_amdgcn_readfirstlane(own);
+}
+
+// Row tile `t` of them: its expert, first row and row count.  False where t is
+// past the last one.
 __device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, int BM, int t,
                                          int& e, int& row0, int& nrows) {
   if (!offsets) {
@@ -124,15 +139,14 @@ __device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, i
       const int o = __shfl_up(upto, d, 64);
       if (lane >= d) upto += o;
     }
-    const int total = __shfl(upto, 63, 64);
+    const int total = __builtin_amdgcn_readlane(upto, 63);
     if (t < total) {
       const int src = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-      const int first = __shfl(upto - own, src, 64);
-      const int slo = __shfl(lo, src, 64), sn = __shfl(n, src, 64);
-      e = __builtin_amdgcn_readfirstlane(e0 + src);
-      row0 = __builtin_amdgcn_readfirstlane(slo + (t - first) * BM);
-      const int left = sn - (t - first) * BM;
-      nrows = __builtin_amdgcn_readfirstlane(left < BM ? left : BM);
+      const int first = __builtin_amdgcn_readlane(upto - own, src);
+      e = e0 + src;
+      row0 = __builtin_amdgcn_readlane(lo, src) + (t - first) * BM;
+      const int left = __builtin_amdgcn_readlane(n, src) - (t - first) * BM;
+      nrows = left < BM ? left : BM;
       return true;
     }
     t -= total;
@@ -149,12 +163,45 @@ __device__ __forceinline__ int source_row(const ProductArgs& g, int s) {
   return r < g.R ? r : -1;
 }
 
+// Four neighbouring elements at a multiple of four, of an aligned array.
+__device__ __forceinline__ f32x4 load4_as_f32(const void* p, int64_t i, int type) {
+  if (type == kF32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  const uint16_t h[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
+  f32x4 o;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) o[r] = type == kBf16 ? Bf16::to_f32(h[r]) : F16::to_f32(h[r]);
+  return o;
+}
+__device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int type, const f32x4& v) {
+  if (type == kF32) {
+    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+    return;
+  }
+  uint32_t h[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) h[r] = type == kBf16 ? Bf16::from_f32(v[r]) : F16::from_f32(v[r]);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+}
+
 // What a product does with the sums of one row's columns j .. j + 3: bias, the
 // kept pre-activation, activation, residual and accumulation in fp32, then one
 // rounding to the result's type.  The activation takes the sum itself, not its
-// rounded copy z.  `wide`: every array allows 4 elements at once.
+// rounded copy z.  g.wide: every array takes four columns in one access.
 __device__ __forceinline__ void finish4(const ProductArgs& g, void* c, int64_t i, int j,
                                         const f32x4& sum) {
+  if (g.wide) {
+    f32x4 v = sum;
+    if (g.bias) v += load4_as_f32(g.bias, j, g.bias_type);
+    if (g.z) store4_from_f32(g.z, i * g.ldz + j, g.type, v);
+    if (g.act != kActNone)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = activate(v[r], g.act);
+    if (g.residual) v += load4_as_f32(g.residual, i * g.ldr + j, g.c_type);
+    if (g.accumulate) v += load4_as_f32(c, i * g.ldc + j, g.c_type);
+    store4_from_f32(c, i * g.ldc + j, g.c_type, v);
+    return;
+  }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     if (j + r >= g.J) break;

@@ -23,6 +23,10 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 __device__ __forceinline__ void lds_load16(uint32_t lds_base, const void* g) {
   asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(g), "{m0}"(lds_base) : "memory");
 }
+// The same from a uniform base and a lane's byte offset (unsigned 32 bits).
+__device__ __forceinline__ void lds_load16_at(uint32_t lds_base, const void* base, uint32_t off) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds_base) : "memory");
+}
 // The same with the non-temporal hint, for data read once (weights): the L2
 // keeps it at low priority, so reused activation rows stay resident.
 __device__ __forceinline__ void lds_load16_nt(uint32_t lds_base, const void* g) {

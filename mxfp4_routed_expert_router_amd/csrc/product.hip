@@ -143,10 +143,15 @@ __global__ void __launch_bounds__(256) product_join_kernel(ProductArgs g, int ch
     finish4(g, g.c, i, j, v);
 }
 
-int64_t row_tiles_most(const ProductArgs& a, int BM) {
-  if (!a.offsets) return (a.P + BM - 1) / BM;
-  const int64_t live = a.E < a.P ? a.E : a.P;  // experts that can have rows
-  return (a.P + live * (BM - 1)) / BM;
+bool product_lds_takes(const ProductArgs& a, int op) {
+  constexpr int64_t kMaxStride = 1 << 22;  // a tile's byte offsets stay within 32 bits
+  const auto ok = [](const uint16_t* p, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && ld <= kMaxStride;
+  };
+  if (!ok(a.a, a.lda) || !ok(a.b, a.ldb) || a.w_stride % 8) return false;
+  if (op == kFwd) return a.K % 8 == 0;
+  if (op == kDgrad) return a.K % 8 == 0 && a.J % 8 == 0;
+  return a.I % 8 == 0 && a.J % 8 == 0;
 }
 
 template <typename T>
@@ -169,7 +174,16 @@ size_t product_workspace(const ProductArgs&, int) { return 0; }
 hipError_t launch_product(ProductArgs a, int op, void*, hipStream_t stream) {
   a.splits = 1;
   if (op != kWgrad && a.P == 0) return hipSuccess;
-  if (a.type == kBf16)
+  const auto four = [](const void* p, int64_t ld, int type) {  // rows take 4 elements at once
+    return !p || ((reinterpret_cast<uintptr_t>(p) & (type == kF32 ? 15 : 7)) == 0 && ld % 4 == 0);
+  };
+  a.wide = a.J % 4 == 0 && four(a.c, a.ldc, a.c_type) && a.c_stride % 4 == 0 &&
+           four(a.bias, 0, a.bias_type) && four(a.residual, a.ldr, a.c_type) && four(a.z, a.ldz, a.type);
+  if (product_lds_takes(a, op)) {
+    if (op == kFwd) launch_product_fwd(a, stream);
+    else if (op == kDgrad) launch_product_dgrad(a, stream);
+    else launch_product_wgrad(a, stream);
+  } else if (a.type == kBf16)
     launch_any<Bf16>(a, op, stream);
   else
     launch_any<F16>(a, op, stream);
