@@ -335,9 +335,9 @@ int moe_fp4_quant_mxfp8(const uint16_t *src, int32_t rows, int32_t K, uint8_t *c
  * host validation before any HIP call, no allocation, no state), with these
  * additions:
  *   - A row stride (ld*) counts elements; 0 means dense rows.  Otherwise it is
- *     at least the row's width (EINVAL).
+ *     at least the row's width and at most 4194304 (EINVAL).
  *   - Arrays need the alignment of their elements only (EALIGN).  Rows that
- *     start on 16-byte boundaries take the faster kernels.
+ *     start on 16-byte boundaries and are a multiple of 8 long run fastest.
  *   - Zero rows (P, M or T = 0) are allowed; arrays of no elements may be NULL.
  *   - Sums are fp32 in a fixed order: the same inputs give the same bits.  Each
  *     result is rounded once, to nearest, ties to even.

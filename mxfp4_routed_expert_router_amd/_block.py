@@ -61,6 +61,26 @@ for _name, _args in (
 
 def _rows(t, name: str, dtypes, device=None, shape=None, ndim: int = 2) -> int:
     """Checks a tensor of rows and returns its row stride in elements (0: dense)."""
+    try:
+        ok = (t.dtype in dtypes and t.is_cuda and t.dim() == ndim and (device is None or t.device == device) and
+              (shape is None or t.shape == shape))
+    except AttributeError:
+        raise TypeError(f"{name} must be a tensor") from None
+    if not ok:
+        _refuse(t, name, dtypes, device, shape, ndim)
+    if t.is_contiguous():
+        return 0
+    st, sz = t.stride(), t.shape
+    if sz[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if ndim == 1 or sz[-2] <= 1:
+        return 0
+    if st[-2] < sz[-1]:
+        raise ValueError(f"{name} has rows that overlap (stride {st[-2]} of {sz[-1]} elements)")
+    return st[-2]
+
+
+def _refuse(t, name, dtypes, device, shape, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
@@ -71,20 +91,7 @@ def _rows(t, name: str, dtypes, device=None, shape=None, ndim: int = 2) -> int:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must be a {ndim}-d tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.is_contiguous():
-        return 0
-    st, sz = t.stride(), t.shape
-    if sz[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-    if ndim == 1:
-        return 0
-    if sz[-2] <= 1:
-        return 0
-    if st[-2] < sz[-1]:
-        raise ValueError(f"{name} has rows that overlap (stride {st[-2]} of {sz[-1]} elements)")
-    return st[-2]
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _experts(t: torch.Tensor, name: str, dtypes, device=None, shape=None):
@@ -119,10 +126,12 @@ def _out_type(dtype, like, name: str = "out_dtype"):
     return dtype
 
 
-def _workspace(fn, *args, workspace, device):
+def _workspace(fn, d, *args, workspace, device):
     """The call's workspace: the given one (checked by the library), or a new one."""
     n = _SZ()
-    _check(fn(*args, ctypes.byref(n)), fn.__name__)
+    rc = fn(d, *args, n)
+    if rc:
+        _check(rc, fn.__name__)
     if workspace is None:
         if n.value == 0:
             return None, 0, None
@@ -135,22 +144,22 @@ def _workspace(fn, *args, workspace, device):
 
 
 class _on:
-    """Launches go to the tensors' device whatever the current one is; costs one
-    comparison where they agree."""
+    """Launches go to the tensors' device whatever the current one is, on its
+    current stream."""
     __slots__ = ("index", "before")
 
     def __init__(self, device):
-        self.index, self.before = device.index, None
+        self.index = device.index
 
     def __enter__(self):
-        now = torch.cuda.current_device()
+        now = torch._C._cuda_getDevice()
+        self.before = now if now != self.index else -1
         if now != self.index:
-            self.before = now
             torch.cuda.set_device(self.index)
-        return torch.cuda.current_stream(self.index).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        if self.before is not None:
+        if self.before >= 0:
             torch.cuda.set_device(self.before)
 
 
@@ -164,7 +173,7 @@ def moe_fp4_grouped_workspace_size(E: int, P: int, N: int, K: int, op: int, dtyp
     """Bytes of workspace of a grouped product; `op` is one of GROUPED_*."""
     d = GroupedDims(E, P, N, K, P, 1, _TYPES[dtype], _TYPES[_out_type(out_dtype, dtype)])
     n = _SZ()
-    _check(_lib.moe_fp4_grouped_workspace_size(ctypes.byref(d), op, ctypes.byref(n)),
+    _check(_lib.moe_fp4_grouped_workspace_size(d, op, n),
            "moe_fp4_grouped_workspace_size")
     return n.value
 
@@ -196,9 +205,9 @@ def moe_fp4_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Ten
     ldy = _rows(y, "y", (_out_type(out_dtype, y.dtype if y.dtype == torch.float32 else x.dtype),), dev, (P, N))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[x.dtype], _TYPES[y.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, ctypes.byref(d), GROUPED_FORWARD,
+        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_FORWARD,
                                    workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_forward(ctypes.byref(d), x.data_ptr(), w.data_ptr(),
+        _check(_lib.moe_fp4_grouped_forward(d, x.data_ptr(), w.data_ptr(),
                                             offsets.data_ptr(), _opt(rows), y.data_ptr(),
                                             ACCUMULATE if accumulate else 0, ws, nws, stream),
                "moe_fp4_grouped_forward")
@@ -225,9 +234,9 @@ def moe_fp4_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tens
     ldx = _rows(dx, "dx", (_out_type(out_dtype, dx.dtype if dx.dtype == torch.float32 else dy.dtype),), dev, (P, K))
     d = GroupedDims(E, P, N, K, P, 1, _TYPES[dy.dtype], _TYPES[dx.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, ctypes.byref(d), GROUPED_DGRAD,
+        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_DGRAD,
                                    workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_dgrad(ctypes.byref(d), dy.data_ptr(), w.data_ptr(),
+        _check(_lib.moe_fp4_grouped_dgrad(d, dy.data_ptr(), w.data_ptr(),
                                           offsets.data_ptr(), dx.data_ptr(),
                                           ACCUMULATE if accumulate else 0, ws, nws, stream),
                "moe_fp4_grouped_dgrad")
@@ -259,9 +268,9 @@ def moe_fp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
                        dev, (E, N, K))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[dy.dtype], _TYPES[dw.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, ctypes.byref(d), GROUPED_WGRAD,
+        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_WGRAD,
                                    workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_wgrad(ctypes.byref(d), dy.data_ptr(), x.data_ptr(),
+        _check(_lib.moe_fp4_grouped_wgrad(d, dy.data_ptr(), x.data_ptr(),
                                           offsets.data_ptr(), _opt(rows), dw.data_ptr(),
                                           ACCUMULATE if accumulate else 0, ws, nws, stream),
                "moe_fp4_grouped_wgrad")
@@ -276,7 +285,7 @@ def moe_fp4_linear_workspace_size(M: int, N: int, K: int, backward: bool = False
     d = LinearDims(M, N, K, t, _TYPES[_out_type(out_dtype, dtype)], t,
                    _TYPES[_out_type(dw_dtype, dtype, "dw_dtype")], act)
     n = _SZ()
-    _check(_lib.moe_fp4_linear_workspace_size(ctypes.byref(d), int(backward), ctypes.byref(n)),
+    _check(_lib.moe_fp4_linear_workspace_size(d, int(backward), n),
            "moe_fp4_linear_workspace_size")
     return n.value
 
@@ -306,9 +315,9 @@ def moe_fp4_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     t = _TYPES[x.dtype]
     d = LinearDims(M, N, K, t, _TYPES[y.dtype], t if bias is None else _TYPES[bias.dtype], t, act, ldx, ldw, ldy, ldr)
     with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, ctypes.byref(d), 0, workspace=workspace,
+        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 0, workspace=workspace,
                                    device=dev)
-        _check(_lib.moe_fp4_linear(ctypes.byref(d), x.data_ptr(), w.data_ptr(), _opt(bias), _opt(residual),
+        _check(_lib.moe_fp4_linear(d, x.data_ptr(), w.data_ptr(), _opt(bias), _opt(residual),
                                    y.data_ptr(), _opt(z), ACCUMULATE if accumulate else 0, ws, nws, stream),
                "moe_fp4_linear")
     return (y, z) if save_z else y
@@ -365,9 +374,9 @@ def moe_fp4_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opti
     d = LinearDims(M, N, K, t, _TYPES[dy.dtype], t, t if dw is None else _TYPES[dw.dtype], act, ldx, ldw, ldy, 0, ldz,
                    lddx, lddw)
     with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, ctypes.byref(d), 1, workspace=workspace,
+        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 1, workspace=workspace,
                                    device=dev)
-        _check(_lib.moe_fp4_linear_backward(ctypes.byref(d), dy.data_ptr(), _opt(x), _opt(w), _opt(z), _opt(dx),
+        _check(_lib.moe_fp4_linear_backward(d, dy.data_ptr(), _opt(x), _opt(w), _opt(z), _opt(dx),
                                             _opt(dw), _opt(db), ACCUMULATE if accumulate else 0, ws, nws, stream),
                "moe_fp4_linear_backward")
     return dx, dw, db
@@ -414,14 +423,14 @@ def moe_fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Op
             mean = torch.empty(T, dtype=torch.float32, device=dev)
     d = NormDims(T, H, _TYPES[x.dtype], _TYPES[y.dtype], _TYPES[wt], kind, eps, ldx, ldy)
     with _on(dev) as stream:
-        _check(_lib.moe_fp4_norm(ctypes.byref(d), x.data_ptr(), _opt(gamma), _opt(beta), y.data_ptr(), _opt(mean),
+        _check(_lib.moe_fp4_norm(d, x.data_ptr(), _opt(gamma), _opt(beta), y.data_ptr(), _opt(mean),
                                  _opt(rstd), stream), "moe_fp4_norm")
     return (y, mean, rstd) if save_stats else y
 
 
 def moe_fp4_norm_backward_workspace_size(T: int, H: int) -> int:
     n = _SZ()
-    _check(_lib.moe_fp4_norm_backward_workspace_size(ctypes.byref(NormDims(T, H)), ctypes.byref(n)),
+    _check(_lib.moe_fp4_norm_backward_workspace_size(NormDims(T, H), n),
            "moe_fp4_norm_backward_workspace_size")
     return n.value
 
@@ -470,9 +479,9 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
     with _on(dev) as stream:
         ws, nws, keep = None, 0, None
         if need_dgamma or need_dbeta:
-            ws, nws, keep = _workspace(_lib.moe_fp4_norm_backward_workspace_size, ctypes.byref(d),
+            ws, nws, keep = _workspace(_lib.moe_fp4_norm_backward_workspace_size, d,
                                        workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_norm_backward(ctypes.byref(d), dy.data_ptr(), x.data_ptr(), _opt(gamma), _opt(mean),
+        _check(_lib.moe_fp4_norm_backward(d, dy.data_ptr(), x.data_ptr(), _opt(gamma), _opt(mean),
                                           rstd.data_ptr(), _opt(dx), _opt(dgamma), _opt(dbeta),
                                           ACCUMULATE if accumulate else 0, ws, nws, stream), "moe_fp4_norm_backward")
     return dx, dgamma, dbeta

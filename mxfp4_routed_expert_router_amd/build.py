@@ -14,7 +14,8 @@ MEASURE_LIB = os.path.join(HERE, "libmoe_fp4_measure.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.hip", "route.hip", "router.hip", "decode.hip", "prefill.hip", "prefill_lds.hip", "mx8.hip", "shared.hip", "stack.hip",
            "api_block.hip", "product.hip", "product_fwd.hip", "product_dgrad.hip",
-           "product_wgrad.hip", "slope.hip", "norm.hip"]
+           "product_wgrad.hip", "product_few.hip", "product_row.hip",
+           "slope.hip", "norm.hip"]
 
 # Packed fp32 VALU ops are switched off for all device code (the host pass warns
 # that it does not know the feature; that is harmless).

@@ -27,10 +27,12 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) &
 size_t size_of(int type) { return type == kF32 ? 4 : 2; }
 bool type_ok(int t) { return t == kF32 || t == kBf16 || t == kF16; }
 bool is16(int t) { return t == kBf16 || t == kF16; }
-// A row stride as given (0: dense); false where rows would overlap.
+// A row stride as given (0: dense); false where rows would overlap, or where a
+// tile's byte offsets would not fit the kernels' 32 bits.
+constexpr int64_t kMaxRowStride = 1 << 22;
 bool stride(int64_t given, int width, int64_t& ld) {
   ld = given ? given : width;
-  return ld >= width && ld <= (int64_t)1 << 40;
+  return ld >= width && ld <= kMaxRowStride;
 }
 int workspace_check(const void* ws, size_t have, size_t need) {
   if (need == 0) return MOE_FP4_OK;

@@ -48,16 +48,21 @@ struct ProductArgs {
   // [I][J] (wgrad [E][I][J]); 1: none
   int splits;
   float* part;
-  int wide;                // set by launch_product: the epilogue takes four columns at a time
+  // set by launch_product: the epilogue takes four columns at a time; it only rounds
+  int wide, plain;
 };
 
 size_t product_workspace(const ProductArgs& a, int op);  // bytes of `part`
 hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream);
-// The products through LDS tiles filled straight from memory, for 16-byte
-// aligned rows whose length is a multiple of 8 (product_lds_takes).
-void launch_product_fwd(const ProductArgs& a, hipStream_t stream);
-void launch_product_dgrad(const ProductArgs& a, hipStream_t stream);
-void launch_product_wgrad(const ProductArgs& a, hipStream_t stream);
+// The tile shapes of the products through LDS.  kAny takes rows of any length and
+// alignment, the others 16-byte aligned rows whose length is a multiple of 8.
+enum { kBig, kMid, kLow, kAny };
+void launch_product_fwd(const ProductArgs& a, int shape, hipStream_t stream);
+void launch_product_dgrad(const ProductArgs& a, int shape, hipStream_t stream);
+void launch_product_wgrad(const ProductArgs& a, int shape, hipStream_t stream);
+// Forward for up to m = 1, 2 or 4 rows a tile, and for 16.
+void launch_product_row(const ProductArgs& a, int m, hipStream_t stream);
+void launch_product_few(const ProductArgs& a, hipStream_t stream);
 // The most row tiles of BM rows that the experts can have.
 inline int64_t row_tiles_most(const ProductArgs& a, int BM) {
   if (!a.offsets) return (a.P + BM - 1) / BM;

@@ -154,6 +154,23 @@ __device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, i
   return false;
 }
 
+// Eight elements at any element's address: p[0 .. n - 1], zeros behind (n <= 0:
+// nothing is read).  The hardware takes 16-byte loads at any address.
+typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
+  if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
+  u32x4 o = zero4();
+#pragma unroll
+  for (int i = 0; i < 7; ++i)
+    if (i < n) o[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+  return o;
+}
+
+// All eight, of data read once (weights): the caches keep it at low priority.
+__device__ __forceinline__ u32x4 load8_once(const uint16_t* p) {
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+}
+
 // Row of x that row s of the ragged side reads, or -1 for a zero row.
 __device__ __forceinline__ int source_row(const ProductArgs& g, int s) {
   if (!g.rows) return s;
@@ -184,10 +201,26 @@ __device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int type, co
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
 }
 
-// What a product does with the sums of one row's columns j .. j + 3: bias, the
-// kept pre-activation, activation, residual and accumulation in fp32, then one
-// rounding to the result's type.  The activation takes the sum itself, not its
-// rounded copy z.  g.wide: every array takes four columns in one access.
+// What a product does with the sums of one row's columns j .. j + N - 1: bias,
+// the kept pre-activation, activation, residual and accumulation in fp32, then
+// one rounding to the result's type.  The activation takes the sum itself, not
+// its rounded copy z.
+template <int N>
+__device__ __forceinline__ void finish_columns(const ProductArgs& g, void* c, int64_t i, int j,
+                                               const f32x4& sum) {
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    if (j + r >= g.J) break;
+    float v = sum[r];
+    if (g.bias) v += load_as_f32(g.bias, j + r, g.bias_type);
+    if (g.z) store_from_f32(g.z, i * g.ldz + j + r, g.type, v);
+    v = activate(v, g.act);
+    if (g.residual) v += load_as_f32(g.residual, i * g.ldr + j + r, g.c_type);
+    if (g.accumulate) v += load_as_f32(c, i * g.ldc + j + r, g.c_type);
+    store_from_f32(c, i * g.ldc + j + r, g.c_type, v);
+  }
+}
+// The same for four columns, in one access of each array where they allow it (g.wide).
 __device__ __forceinline__ void finish4(const ProductArgs& g, void* c, int64_t i, int j,
                                         const f32x4& sum) {
   if (g.wide) {
@@ -202,17 +235,7 @@ __device__ __forceinline__ void finish4(const ProductArgs& g, void* c, int64_t i
     store4_from_f32(c, i * g.ldc + j, g.c_type, v);
     return;
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    if (j + r >= g.J) break;
-    float v = sum[r];
-    if (g.bias) v += load_as_f32(g.bias, j + r, g.bias_type);
-    if (g.z) store_from_f32(g.z, i * g.ldz + j + r, g.type, v);
-    v = activate(v, g.act);
-    if (g.residual) v += load_as_f32(g.residual, i * g.ldr + j + r, g.c_type);
-    if (g.accumulate) v += load_as_f32(c, i * g.ldc + j + r, g.c_type);
-    store_from_f32(c, i * g.ldc + j + r, g.c_type, v);
-  }
+finish_columns<4>(g, c, i, j, sum);
 }
 __device__ __forceinline__ void* result_of(const ProductArgs& g, int e) {
   return static_cast<char*>(g.c) + (int64_t)e * g.c_stride * (g.c_type == kF32 ? 4 : 2);

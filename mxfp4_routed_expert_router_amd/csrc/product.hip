@@ -1,124 +1,12 @@
-// 16-bit products grouped by expert (and dense, as one expert) on the matrix cores.
+// 16-bit products grouped by expert, and dense as one expert: which kernel runs,
+// and the joining of split sums.
 #include "block_device.h"
 
 namespace moe_fp4 {
 namespace {
 
-// ---------------------------------------------------------------- any sizes, any alignment
-// 64 x 64 results a workgroup of four waves (32 x 32 each), 32 of the sum at a
-// time through LDS as [index][k].  Elements are loaded one by one where a row
-// is not 16-byte aligned or ends inside a chunk, so every size and stride runs
-// here.
-constexpr int kAnyTile = 64, kAnyK = 32, kAnyPad = 40;
-
-// Eight elements p[0..7], those from n on as zeros.
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, int n, bool wide) {
-  if (n >= 8 && wide) return ld16(p);
-  uint16_t v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0;
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = (uint32_t)v[2 * i] | ((uint32_t)v[2 * i + 1] << 16);
-  return o;
-}
-
-template <typename T, int OP>
-__global__ void __launch_bounds__(256) product_any_kernel(ProductArgs g, int row_tiles, int col_tiles) {
-  __shared__ __align__(16) uint16_t sa[kAnyTile * kAnyPad], sb[kAnyTile * kAnyPad];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int ct = blockIdx.x % col_tiles, rt = blockIdx.x / col_tiles;
-  int e, row0 = 0, nrows = 0, i0, j0 = ct * kAnyTile, ni, klen;
-  const uint16_t* b = g.b;
-  if (OP == kWgrad) {
-    e = rt / row_tiles;
-    i0 = (rt % row_tiles) * kAnyTile;
-    ni = g.I - i0;
-    segment(g.offsets, e, g.P, row0, klen);
-  } else {
-    if (!row_tile(g.offsets, g.E, g.P, kAnyTile, rt, e, row0, nrows)) return;
-    i0 = row0;
-    ni = nrows;
-    klen = g.K;
-    b += (int64_t)e * g.w_stride;
-  }
-  // this workgroup's part of the sum
-  int k0 = 0, k1 = klen;
-  if (g.splits > 1) {
-    const int per = ((klen + g.splits - 1) / g.splits + kAnyK - 1) / kAnyK * kAnyK;
-    k0 = (int)blockIdx.y * per;
-    k1 = k0 + per < klen ? k0 + per : klen;
-  }
-  const bool wa = (((uintptr_t)g.a | (uintptr_t)(g.lda * 2)) & 15) == 0;
-  const bool wb = (((uintptr_t)b | (uintptr_t)(g.ldb * 2)) & 15) == 0;
-  // along k: thread t loads index t / 4, k chunk t % 4; along the index: k t / 8, index chunk t % 8
-  const int kr = t >> 2, kc = (t & 3) * 8, sr = t >> 3, sc = (t & 7) * 8;
-  int64_t arow = -1;
-  if (OP == kFwd && kr < ni) {
-    const int s = source_row(g, i0 + kr);
-    if (s >= 0) arow = (int64_t)s * g.lda;
-  }
-  if (OP == kDgrad && kr < ni) arow = (int64_t)(i0 + kr) * g.lda;
-  f32x4 acc[2][2] = {};
-  for (int k = k0; k < k1; k += kAnyK) {
-    u32x4 va = zero4(), vb = zero4();
-    if (OP != kWgrad) {
-      if (arow >= 0) va = load8(g.a + arow + k + kc, k1 - k - kc, wa);
-    } else if (k + sr < k1) {
-      va = load8(g.a + (int64_t)(row0 + k + sr) * g.lda + i0 + sc, g.I - i0 - sc, wa);
-    }
-    if (OP == kFwd) {
-      if (j0 + kr < g.J) vb = load8(b + (int64_t)(j0 + kr) * g.ldb + k + kc, k1 - k - kc, wb);
-    } else if (k + sr < k1) {
-      const int s = OP == kWgrad ? source_row(g, row0 + k + sr) : k + sr;
-      if (s >= 0) vb = load8(b + (int64_t)s * g.ldb + j0 + sc, g.J - j0 - sc, wb);
-    }
-    __syncthreads();  // the previous step's reads are done
-    if (OP != kWgrad) {
-      st16(sa + kr * kAnyPad + kc, va);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sa[(sc + i) * kAnyPad + sr] = (uint16_t)(va[i / 2] >> (16 * (i & 1)));
-    }
-    if (OP == kFwd) {
-      st16(sb + kr * kAnyPad + kc, vb);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sb[(sc + i) * kAnyPad + sr] = (uint16_t)(vb[i / 2] >> (16 * (i & 1)));
-    }
-    __syncthreads();
-    u32x4 fa[2], fb[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      fa[x] = ld16(sa + ((wave & 1) * 32 + x * 16 + (lane & 15)) * kAnyPad + (lane >> 4) * 8);
-      fb[x] = ld16(sb + ((wave >> 1) * 32 + x * 16 + (lane & 15)) * kAnyPad + (lane >> 4) * 8);
-    }
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) acc[y][x] = T::mfma(fb[y], fa[x], acc[y][x]);
-  }
-  // B's rows are the matrix instruction's A operand: a lane holds four
-  // neighbouring columns of one result row
-  void* c = OP == kWgrad ? result_of(g, e) : g.c;
-#pragma unroll
-  for (int y = 0; y < 2; ++y)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int di = (wave & 1) * 32 + x * 16 + (lane & 15);
-      const int j = j0 + (wave >> 1) * 32 + y * 16 + (lane >> 4) * 4;
-      if (di >= ni || j >= g.J) continue;
-      if (g.splits > 1) {
-        const int64_t slice = (int64_t)blockIdx.y * (OP == kWgrad ? g.E : 1) + (OP == kWgrad ? e : 0);
-        float* p = g.part + (slice * g.I + i0 + di) * g.J + j;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (j + r < g.J) p[r] = acc[y][x][r];
-      } else {
-        finish4(g, c, i0 + di, j, acc[y][x]);
-      }
-    }
-}
+constexpr int kSumStep = 64;
+constexpr double kMaxParts = 256e6;  // bytes of a split sum's parts
 
 // The parts of a split sum, added in order, then the epilogue.  Four columns a
 // thread.  Rows that no expert owns are left alone.
@@ -133,9 +21,13 @@ __global__ void __launch_bounds__(256) product_join_kernel(ProductArgs g, int ch
   f32x4 v = {};
   for (int s = 0; s < g.splits; ++s) {
     const float* p = g.part + ((int64_t)s * rows + i) * g.J + j;
+    if (g.J % 4 == 0) {
+      v += *reinterpret_cast<const f32x4*>(p);
+    } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (j + r < g.J) v[r] += p[r];
+      for (int r = 0; r < 4; ++r)
+        if (j + r < g.J) v[r] += p[r];
+    }
   }
   if (OP == kWgrad)
     finish4(g, result_of(g, (int)(i / g.I)), i % g.I, j, v);
@@ -143,10 +35,10 @@ __global__ void __launch_bounds__(256) product_join_kernel(ProductArgs g, int ch
     finish4(g, g.c, i, j, v);
 }
 
-bool product_lds_takes(const ProductArgs& a, int op) {
-  constexpr int64_t kMaxStride = 1 << 22;  // a tile's byte offsets stay within 32 bits
+// Whether both operands' rows are 16-byte aligned and a multiple of 8 long.
+bool wide_rows(const ProductArgs& a, int op) {
   const auto ok = [](const uint16_t* p, int64_t ld) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0 && ld <= kMaxStride;
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0;
   };
   if (!ok(a.a, a.lda) || !ok(a.b, a.ldb) || a.w_stride % 8) return false;
   if (op == kFwd) return a.K % 8 == 0;
@@ -154,39 +46,176 @@ bool product_lds_takes(const ProductArgs& a, int op) {
   return a.I % 8 == 0 && a.J % 8 == 0;
 }
 
-template <typename T>
-void launch_any(const ProductArgs& a, int op, hipStream_t stream) {
-  const int ct = (a.J + kAnyTile - 1) / kAnyTile;
-  const int it = (a.I + kAnyTile - 1) / kAnyTile;
-  const int64_t rt = op == kWgrad ? (int64_t)it * a.E : row_tiles_most(a, kAnyTile);
-  const dim3 grid((unsigned)(rt * ct), (unsigned)a.splits);
-  switch (op) {
-    case kFwd: hipLaunchKernelGGL((product_any_kernel<T, kFwd>), grid, dim3(256), 0, stream, a, it, ct); break;
-    case kDgrad: hipLaunchKernelGGL((product_any_kernel<T, kDgrad>), grid, dim3(256), 0, stream, a, it, ct); break;
-    default: hipLaunchKernelGGL((product_any_kernel<T, kWgrad>), grid, dim3(256), 0, stream, a, it, ct); break;
+// How a product runs, from its sizes alone.
+struct Tiles {
+  double us;   // estimated time
+  int shape;   // where the rows allow it (kAny otherwise)
+  int splits;  // of the sum
+};
+struct Plan {
+  int rows;         // forward: 1, 2 or 4 rows a wave, 16 for the few-row kernel, 0 for tiles
+  int cut;          // tiles: columns of the first launch; the others take `rest`
+  Tiles main, rest;
+};
+
+// The tile shape and the number of parts of the sum that come out fastest for J
+// columns, by these measurements (us for a step of 64 of the sum, bf16, K = 5120;
+// the forms differ by a few percent):
+//   Big 256 x 256   up to 128 workgroups 1.2, 256: 1.6, 512: 3.1, 768: 4.6
+//   Mid 128 x 128   up to 256: 0.6, 512: 1.0, 768: 1.45, 1024: 1.9
+//   Low 64 x 128    up to 256: 0.54, 512: 0.68, 768: 1.0, 1024: 1.37
+// So Big goes in rounds of one workgroup a CU, the others flow.  A ragged tile
+// with few rows takes less; the weights of all experts take their bytes' time
+// whatever the shape (48 experts of 2304 x 5120, 8, 32, 128 and 256 rows each:
+// Big 205, 209, 275, 391 us; Mid 201, 216, 297, 505; Low 226, 237, 386, 625).
+// Splitting the sum adds a launch and the parts' way to memory and back.
+Tiles best_tiles(const ProductArgs& a, int op, int J) {
+  static const struct { int bi, bj, occ; double us[3], thin; } kShapes[3] = {
+      {256, 256, 1, {1.6, 1.6, 1.6}, 0.45}, {128, 128, 2, {0.6, 1.0, 1.0}, 0.5}, {64, 128, 3, {0.54, 0.68, 1.0}, 0.6}};
+  const int64_t live = !a.offsets ? 1 : a.E < a.P ? a.E : a.P > 0 ? a.P : 1;
+  const int64_t groups = op == kWgrad ? a.E : live;               // experts with results
+  const double rows = op == kWgrad ? a.I : (double)a.P / groups;  // of one, on average
+  const double sum = op == kWgrad ? (double)a.P / live : a.K;     // its length
+  const bool ragged = op != kWgrad && a.offsets;
+  const double results = (double)(op == kWgrad ? (int64_t)a.E * a.I : a.I) * J;
+  const double memory = (op == kWgrad ? results * 2 : (double)live * a.K * J * 2) / 5.2e6;
+  Tiles best{1e30, kLow, 1};
+  for (int s = 0; s < 3; ++s) {
+    const auto& h = kShapes[s];
+    const double ct = (J + h.bj - 1) / h.bj;
+    double tiles;
+    if (!ragged) {
+      tiles = ct * groups * (((int64_t)rows + h.bi - 1) / h.bi);
+    } else {  // half a tile more than the rows fill, on average
+      const double nt = rows / h.bi + 0.5 > 1 ? rows / h.bi + 0.5 : 1;
+      tiles = ct * groups * (h.thin * nt + (1 - h.thin) * rows / h.bi);
+    }
+    for (int n = 1; n <= 16; n *= 2) {
+      const int64_t steps = (int64_t)(sum / n + kSumStep - 1) / kSumStep;
+      if (n > 1 && (steps < 4 || results * 4 * n > kMaxParts)) break;
+      const double wgs = tiles * n, at = 256.0 * h.occ, rounds = wgs / at;
+      double step;
+      if (s == kBig && !ragged) {
+        const double whole = (double)(int64_t)rounds, rest = wgs - whole * at;
+        step = 1.6 * whole + (rest > 128 ? 1.6 : rest > 0 ? 1.2 : 0);
+      } else {
+        step = rounds > 1 ? rounds * h.us[h.occ - 1] : h.us[wgs <= 256 ? 0 : wgs <= 512 ? 1 : 2];
+      }
+      double us = step * (steps + 3);
+      if (us < memory) us = memory;
+      if (n > 1) us += 6.0 + 2 * n * results * 4 / 4e6;
+      if (us < best.us * 0.97) best = {us, s, n};
+    }
+  }
+  return best;
+}
+
+Plan plan(const ProductArgs& a, int op) {
+  Plan p{};
+  if (op == kFwd) {
+    // one to four rows: the weights once, straight to registers.  Grouped up to
+    // one row an expert on average: 96 rows on 48 of 138 experts 199 us, tiles
+    // 235; 192 on 69: 335, 313.
+    if (a.offsets ? a.P <= a.E : a.P <= 4) {
+      p.rows = a.offsets ? (a.P <= 8 ? 1 : 4) : a.P <= 2 ? a.P : 4;
+      return p;
+    }
+    if (!a.offsets && a.P <= 16) {
+      p.rows = 16;
+      return p;
+    }
+  }
+  p.main = best_tiles(a, op, a.J);
+  p.cut = a.J;
+  // A dense product's last round of Big tiles may leave most CUs idle: the
+  // columns of the whole rounds go first, the others in a launch of their own
+  // (2048 x 9216 x 5120, 288 tiles: 216 us at once).
+  if (!a.offsets) {
+    const int64_t rt = (a.I + 255) / 256, ct = (a.J + 255) / 256, rounds = rt * ct / 256;
+    const int cut = (int)(rounds * 256 / rt) * 256;
+    if (rounds >= 1 && cut > 0 && cut < a.J) {
+      const Tiles rest = best_tiles(a, op, a.J - cut);
+      const double us = 1.6 * rounds * (double)((a.K + kSumStep - 1) / kSumStep + 3) + rest.us;
+      if (us < p.main.us * 0.97) {
+        p.main = {us, kBig, 1};
+        p.rest = rest;
+        p.cut = cut;
+      }
+    }
+  }
+  return p;
+}
+
+// The product's columns from j0 on, n of them.
+ProductArgs columns(const ProductArgs& a, int op, int j0, int n) {
+  ProductArgs r = a;
+  const auto shift = [&](const void* p, int type) -> const void* {
+    return p ? static_cast<const char*>(p) + (int64_t)j0 * (type == kF32 ? 4 : 2) : nullptr;
+  };
+  r.J = n;
+  r.b = a.b + (op == kFwd ? j0 * a.ldb : j0);
+  r.c = const_cast<void*>(shift(a.c, a.c_type));
+  r.bias = shift(a.bias, a.bias_type);
+  r.residual = shift(a.residual, a.c_type);
+  r.z = const_cast<void*>(shift(a.z, a.type));
+  return r;
+}
+
+size_t part_bytes(const ProductArgs& a, int op, int J, int splits) {
+  return splits <= 1 ? 0 : (size_t)splits * (op == kWgrad ? (size_t)a.E * a.I : (size_t)a.I) * J * 4;
+}
+
+void launch_tiles(ProductArgs a, int op, const Tiles& t, hipStream_t stream) {
+  a.splits = t.splits;
+  const int shape = wide_rows(a, op) ? t.shape : kAny;
+  if (op == kFwd)
+    launch_product_fwd(a, shape, stream);
+  else if (op == kDgrad)
+    launch_product_dgrad(a, shape, stream);
+  else
+    launch_product_wgrad(a, shape, stream);
+  if (a.splits > 1) {
+    const int chunks = (a.J + 3) / 4;
+    const int64_t threads = (op == kWgrad ? (int64_t)a.E : 1) * a.I * chunks;
+    const dim3 grid((unsigned)((threads + 255) / 256));
+    if (op == kWgrad)
+      hipLaunchKernelGGL(product_join_kernel<kWgrad>, grid, dim3(256), 0, stream, a, chunks);
+    else
+      hipLaunchKernelGGL(product_join_kernel<kFwd>, grid, dim3(256), 0, stream, a, chunks);
   }
 }
 
 }  // namespace
 
-size_t product_workspace(const ProductArgs&, int) { return 0; }
+size_t product_workspace(const ProductArgs& a, int op) {
+  if (op != kWgrad && a.P == 0) return 0;
+  const Plan p = plan(a, op);
+  if (p.rows) return 0;
+  const size_t m = part_bytes(a, op, p.cut, p.main.splits), r = part_bytes(a, op, a.J - p.cut, p.rest.splits);
+  return m > r ? m : r;
+}
 
-hipError_t launch_product(ProductArgs a, int op, void*, hipStream_t stream) {
-  a.splits = 1;
+hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream) {
   if (op != kWgrad && a.P == 0) return hipSuccess;
   const auto four = [](const void* p, int64_t ld, int type) {  // rows take 4 elements at once
     return !p || ((reinterpret_cast<uintptr_t>(p) & (type == kF32 ? 15 : 7)) == 0 && ld % 4 == 0);
   };
   a.wide = a.J % 4 == 0 && four(a.c, a.ldc, a.c_type) && a.c_stride % 4 == 0 &&
            four(a.bias, 0, a.bias_type) && four(a.residual, a.ldr, a.c_type) && four(a.z, a.ldz, a.type);
-  if (product_lds_takes(a, op)) {
-    if (op == kFwd) launch_product_fwd(a, stream);
-    else if (op == kDgrad) launch_product_dgrad(a, stream);
-    else launch_product_wgrad(a, stream);
-  } else if (a.type == kBf16)
-    launch_any<Bf16>(a, op, stream);
-  else
-    launch_any<F16>(a, op, stream);
+  a.plain = a.wide && !a.bias && !a.residual && !a.z && !a.accumulate && a.act == kActNone;
+  a.part = static_cast<float*>(ws);
+  a.splits = 1;
+  const Plan p = plan(a, op);
+  if (p.rows == 16) {
+    launch_product_few(a, stream);
+  } else if (p.rows) {
+    launch_product_row(a, p.rows, stream);
+  } else if (p.cut == a.J) {
+    launch_tiles(a, op, p.main, stream);
+  } else {
+    launch_tiles(columns(a, op, 0, p.cut), op, p.main, stream);
+    launch_tiles(columns(a, op, p.cut, a.J - p.cut), op, p.rest, stream);
+  }
   return hipGetLastError();
 }
 

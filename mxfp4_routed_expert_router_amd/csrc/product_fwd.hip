@@ -2,24 +2,12 @@
 #include "product_lds.h"
 
 namespace moe_fp4 {
-namespace {
 
-template <typename T>
-void launch(const ProductArgs& a, hipStream_t stream) {
-  switch (product_shape(a, kFwd)) {
-    case kBig: return launch_shape<T, kFwd, Big>(a, stream);
-    case kMid: return launch_shape<T, kFwd, Mid>(a, stream);
-    default: return launch_shape<T, kFwd, Low>(a, stream);
-  }
-}
-
-}  // namespace
-
-void launch_product_fwd(const ProductArgs& a, hipStream_t stream) {
+void launch_product_fwd(const ProductArgs& a, int shape, hipStream_t stream) {
   if (a.type == kBf16)
-    launch<Bf16>(a, stream);
+    launch_tiles<Bf16, kFwd, 3>(a, shape, stream);
   else
-    launch<F16>(a, stream);
+    launch_tiles<F16, kFwd, 3>(a, shape, stream);
 }
 
 }  // namespace moe_fp4

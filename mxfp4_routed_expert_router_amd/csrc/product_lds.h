@@ -1,20 +1,23 @@
 // 16-bit products through LDS tiles filled straight from memory.
 //
 // A workgroup computes BI x BJ results (i: rows of the result, j: its columns),
-// 32 of the sum a step.  A ring of stages in LDS holds the next steps' operand
-// tiles; global_load_lds_dwordx4 fills them without passing through registers,
-// and the fragments of step t + 1 are read from LDS while the matrix
-// instructions of step t run, so the matrix cores wait only at one barrier a
-// step.
+// 64 of the sum a step.  global_load_lds_dwordx4 fills the operands' stages in
+// LDS without passing through registers; the two halves of a step are read into
+// registers half a step ahead of the matrix instructions, and one barrier a
+// step keeps the waves together.  A has two stages, B two or three: B's rows
+// (the weights, in forward and dgrad) come from HBM and are sent for two steps
+// ahead with three.
 //
 // LDS layout.  An operand that is contiguous along the sum (x, dy as the row
-// side, w of forward) is held as [index][32]: 64-byte rows, the 16-byte chunk
-// c of row r at slot c ^ chunk_swizzle(r), so that the 16 rows of a fragment
-// read spread over all banks.  An operand that is contiguous along its own
-// index (w of dgrad; both of wgrad) is held as it lies, [32][index], and
-// ds_read_b64_tr_b16 turns 4 x 16 blocks on the way to the registers: within 16
-// lanes, lane i receives column i of the four rows that lanes 4 r .. 4 r + 3
-// address.  Its 32-byte units (16 indexes) of row r sit at unit ^ unit_swizzle(r).
+// side, w of forward) is held as [index][64]: a load brings whole 128-byte lines
+// (with 64 bytes a row, twice the requests reach the L2), and the 16-byte chunk
+// c of row r lies at c ^ (r % 8), so that a fragment's 16 rows are read without
+// bank conflicts (4 cycles a wave; measured 8 with c ^ (r % 8) ^ (r / 8)).  An
+// operand that is contiguous along its own index (w of dgrad; both of wgrad) is
+// held as it lies, [64][index], and ds_read_b64_tr_b16 turns 4 x 16 blocks on the
+// way to the registers: within 16 lanes, lane i receives column i of the four
+// rows that lanes 4 r .. 4 r + 3 address.  Its 32-byte units (16 indexes) of row
+// r sit at unit ^ unit_swizzle(r).
 #pragma once
 
 #include "block_device.h"
@@ -23,7 +26,7 @@
 namespace moe_fp4 {
 namespace {
 
-constexpr int kStepK = 32;
+constexpr int kStepK = 64;
 constexpr int kIndexCache = 1024;  // row indexes of a gathered sum held in LDS
 
 __device__ const __align__(16) uint32_t zero_chunk[4] = {0u, 0u, 0u, 0u};
@@ -32,49 +35,53 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ int chunk_swizzle(int r) { return ((r >> 1) & 3) ^ ((r >> 3) & 1); }
 // Units of rows r of which 8 (rows 0-3 and 8-11, say) are read together: they
 // take 8 different 32-byte bank groups.
 template <int BX>
 __device__ __forceinline__ int unit_swizzle(int r) {
   if constexpr (BX >= 128) return (r & 3) | ((r >> 1) & 4);
-  if constexpr (BX == 64) return ((r >> 1) & 1) | ((r >> 2) & 2);
-  return (r >> 3) & 1;
+  return ((r >> 1) & 1) | ((r >> 2) & 2);
 }
 
-__device__ __forceinline__ u32x4 lds_read16(uint32_t a) {
-  return *reinterpret_cast<const lds_u32x4*>(a);
+// 16 bytes at a + off, off known when compiling: the instruction's offset.
+__device__ __forceinline__ u32x4 lds_read16(uint32_t a, int off) {
+  return *reinterpret_cast<const lds_u32x4*>(reinterpret_cast<lds_char*>(a) + off);
 }
 // 8 k-values of 16 indexes: two turned 4 x 16 blocks, 4 rows apart.
 template <int BX>
-__device__ __forceinline__ u32x4 lds_read_turned(uint32_t a) {
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(a));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(a + 4 * BX * 2));
+__device__ __forceinline__ u32x4 lds_read_turned(uint32_t a, int off) {
+  lds_char* const p = reinterpret_cast<lds_char*>(a) + off;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(p));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(p + 4 * BX * 2));
   const uint2 l = __builtin_bit_cast(uint2, lo), h = __builtin_bit_cast(uint2, hi);
   return u32x4{l.x, l.y, h.x, h.y};
 }
 
-// BI x BJ results, WI x WJ waves, ST stages; OCC waves per SIMD.
-template <int BI_, int BJ_, int WI_, int WJ_, int ST_, int OCC_>
+// BI x BJ results, WI x WJ waves, SB stages of B; OCC waves per SIMD.
+template <int BI_, int BJ_, int WI_, int WJ_, int SB_, int OCC_>
 struct Shape {
-  static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, ST = ST_, OCC = OCC_;
+  static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, SB = SB_, OCC = OCC_;
   static constexpr int W = WI * WJ, Threads = 64 * W;
-  static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;   // fragments of a wave
-  static constexpr int NI = BI / 16, NJ = BJ / 16;             // 1 KB loads of a stage
-  static constexpr int LPW = (NI + NJ) / W;                    // loads of a wave
-  static constexpr int Stage = (BI + BJ) * 64;
-  // fragments of columns of a pass of the epilogue: at most four, as fit the stages
-  static constexpr int Fit = ST * Stage / (W * FI * 16 * 64);
-  static constexpr int JC = FJ >= 4 && Fit >= 4 ? 4 : FJ >= 2 && Fit >= 2 ? 2 : 1;
-  static_assert((NI + NJ) % W == 0 && ST >= 3, "every wave issues the same number of loads");
+  static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;  // fragments of a wave
+  static constexpr int StageA = BI * 128, StageB = BJ * 128, Lds = 2 * StageA + SB * StageB;
+  static constexpr int LA = BI / 8 / W, LB = BJ / 8 / W;      // 1 KB loads of a wave and stage
+  // the epilogue's passes: up to four fragments of columns by as many of rows as fit the stages
+  static constexpr int JC = FJ < 4 ? FJ : 4, Fit = Lds / (W * 16 * JC * 64), IC = FI <= Fit ? FI : FI / 2;
+  static_assert(BI % (8 * W) == 0 && BJ % (8 * W) == 0 && BI >= 64 && BJ >= 64, "whole loads");
+  static_assert(FJ % JC == 0 && FI % IC == 0 && IC <= Fit, "the epilogue's parts fit the stages");
 };
 
-template <typename T, int OP, bool GATHER, typename S>
+// REG: for rows that are not 16-byte aligned or not a multiple of eight long, the
+// stages (two of each operand) are filled through registers, a step ahead.
+template <typename T, int OP, bool GATHER, bool REG, typename S>
 __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(ProductArgs g, int col_tiles) {
   constexpr bool KA = OP != kWgrad, KB = OP == kFwd;  // contiguous along the sum
-  __shared__ __align__(1024) uint8_t smem[S::ST * S::Stage];
-  __shared__ int32_t index_cache[GATHER && OP == kWgrad ? kIndexCache : 1];
+  constexpr bool RowsA = GATHER && OP == kFwd, RowsB = GATHER && OP == kWgrad;
+  static_assert(!REG || S::SB == 2, "a step ahead");
+  // behind the stages: row indexes of a gathered sum
+  __shared__ __align__(1024) uint8_t smem[S::Lds + (RowsB ? kIndexCache * 4 : 0)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // ---- which tile: workgroups are dealt to the 8 XCDs round robin; each XCD
@@ -116,7 +123,6 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // addresses, a uniform base that advances with the steps and the lane's
   // offset.  Indexes past an edge read the last one's data: their results are
   // not stored.  Gathered rows have 64-bit addresses of their own.
-  constexpr bool RowsA = GATHER && OP == kFwd, RowsB = GATHER && OP == kWgrad;
   const int first = OP == kWgrad ? row0 + k0 : k0;
   const char* const abase = reinterpret_cast<const char*>(
       KA ? g.a + (RowsA ? 0 : (int64_t)i0 * g.lda) + k0 : g.a + (int64_t)first * g.lda + i0);
@@ -124,216 +130,336 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
       KB ? b + (int64_t)j0 * g.ldb + k0 : b + (RowsB ? 0 : (int64_t)first * g.ldb) + j0);
   const int64_t astep = KA ? kStepK * 2 : kStepK * 2 * g.lda, bstep = KB ? kStepK * 2 : kStepK * 2 * g.ldb;
   const char* const zero = reinterpret_cast<const char*>(zero_chunk);
-  const int kchunk = ((lane & 3) ^ chunk_swizzle(lane >> 2)) * 8;  // a lane's place along the sum
-  // turned operands: place along the sum of load u
+  const int kchunk = ((lane & 7) ^ (lane >> 3)) * 8;  // a lane's place along the sum
+  // operands that lie along their index: the place along the sum of load u
   auto krow = [&](int u, int BX) { return u * (512 / BX) + lane / (BX / 8); };
-  uint32_t off[S::LPW];
-  const char* rowp[RowsA ? S::LPW : 1];  // gathered x of forward: the lane's row, or null
-  int src[RowsB ? S::LPW : 1];           // gathered x of wgrad: the lane's row of the step to come, or -1
+  uint32_t offa[S::LA], offb[S::LB];
+  const char* rowp[RowsA ? S::LA : 1];  // gathered x of forward: the lane's row, or null
+  int src[RowsB ? S::LB : 1];           // gathered x of wgrad: the lane's row of the step to come, or -1
 #pragma unroll
-  for (int n = 0; n < S::LPW; ++n) {
-    const int q = n * S::W + wave;
-    const bool isa = q < S::NI;
-    const int u = isa ? q : q - S::NI;
-    if (isa ? KA : KB) {
-      const int r = u * 16 + (lane >> 2), most = isa ? ni : g.J - j0;
-      const int rr = r < most ? r : most - 1;
-      off[n] = (uint32_t)(rr * (isa ? g.lda : g.ldb) + kchunk) * 2;
-      if constexpr (RowsA)
-        if (isa) {
-          const int row = source_row(g, i0 + rr);
-          rowp[n] = row < 0 ? nullptr : abase + ((int64_t)row * g.lda + kchunk) * 2;
-        }
+  for (int n = 0; n < S::LA; ++n) {
+    const int u = n * S::W + wave;
+    if constexpr (KA) {
+      const int r = u * 8 + (lane >> 3), rr = r < ni ? r : ni - 1;
+      offa[n] = (uint32_t)(rr * g.lda + kchunk) * 2;
+      if constexpr (RowsA) {
+        const int row = source_row(g, i0 + rr);
+        rowp[n] = row < 0 ? nullptr : abase + ((int64_t)row * g.lda + kchunk) * 2;
+      }
     } else {
-      const int BX = isa ? S::BI : S::BJ, k = krow(u, BX), s = lane % (BX / 8);
-      const int unit = (s >> 1) ^ (isa ? unit_swizzle<S::BI>(k) : unit_swizzle<S::BJ>(k));
-      const int col = unit * 16 + (s & 1) * 8, most = isa ? g.I - i0 : g.J - j0;
-      off[n] = (uint32_t)((RowsB && !isa ? 0 : k * (isa ? g.lda : g.ldb)) + (col < most ? col : most - 8)) * 2;
+      const int k = krow(u, S::BI), s = lane % (S::BI / 8);
+      const int col = ((s >> 1) ^ unit_swizzle<S::BI>(k)) * 16 + (s & 1) * 8;
+      offa[n] = (uint32_t)(k * g.lda + (col < ni ? col : REG ? 0 : ni - 8)) * 2;
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < S::LB; ++n) {
+    const int u = n * S::W + wave, nj = g.J - j0;
+    if constexpr (KB) {
+      const int r = u * 8 + (lane >> 3);
+      offb[n] = (uint32_t)((r < nj ? r : nj - 1) * g.ldb + kchunk) * 2;
+    } else {
+      const int k = krow(u, S::BJ), s = lane % (S::BJ / 8);
+      const int col = ((s >> 1) ^ unit_swizzle<S::BJ>(k)) * 16 + (s & 1) * 8;
+      offb[n] = (uint32_t)((RowsB ? 0 : k * g.ldb) + (col < nj ? col : REG ? 0 : nj - 8)) * 2;
     }
   }
   const uint32_t lds0 = lds_addr(smem);
-  // Load n of step s.  Past the end of the sum it brings zeros, so that every
-  // step issues the same number of loads and the waits below are exact.
-  auto issue = [&](int n, int s) {
-    const int q = n * S::W + wave;
-    const bool isa = q < S::NI;
-    const uint32_t to = lds0 + (uint32_t)((s % S::ST) * S::Stage + q * 1024);
-    const char* const base = isa ? abase + s * astep : bbase + s * bstep;
-    const int u = isa ? q : q - S::NI;
-    const int k = (isa ? KA : KB) ? kchunk : krow(u, isa ? S::BI : S::BJ);
-    const bool past = s >= full && s * kStepK + k >= klen;
-    if (RowsA && isa) {
-      lds_load16(to, past || !rowp[RowsA ? n : 0] ? zero : rowp[RowsA ? n : 0] + s * astep);
-    } else if (RowsB && !isa) {
-      const int row = src[RowsB ? n : 0];  // -1 past the end
-      lds_load16(to, row < 0 ? zero : bbase + (int64_t)row * g.ldb * 2 + off[n]);
-    } else if (s < full) {
-      lds_load16_at(to, base, off[n]);
+  // Load n of step s of A or B into the stage at `to`.  TAIL: the step may end
+  // or lie past the end of the sum, where zeros are brought in.
+  auto issue_a = [&](int n, int s, uint32_t to, auto tail_) {
+    constexpr bool tail = decltype(tail_)::value != 0;
+    const int u = n * S::W + wave;
+    const bool past = tail && s * kStepK + (KA ? kchunk : krow(u, S::BI)) >= klen;
+    const char* const base = abase + s * astep;
+    if constexpr (RowsA) {
+      const char* const p = rowp[n];
+      lds_load16(to + u * 1024, past || !p ? zero : p + s * astep);
+    } else if constexpr (!tail) {
+      lds_load16_at(to + u * 1024, base, offa[n]);
     } else {
-      lds_load16(to, past ? zero : base + off[n]);
+      lds_load16(to + u * 1024, past ? zero : base + offa[n]);
     }
   };
-  // Gathered sums: a block of row indexes is put into LDS every kIndexCache rows.
-  auto fetch_indexes = [&](int s) {  // before step s's, s * 32 a multiple of kIndexCache
-    for (int i = threadIdx.x; i < kIndexCache; i += S::Threads) {
-      const int k = s * kStepK + i;
-      index_cache[i] = k < klen ? source_row(g, row0 + k0 + k) : -1;
-    }
-    __syncthreads();
-  };
-  auto next_rows = [&](int s) {
-#pragma unroll
-    for (int n = 0; n < S::LPW; ++n)
-      if (n * S::W + wave >= S::NI)
-        src[RowsB ? n : 0] = index_cache[(s * kStepK + krow(n * S::W + wave - S::NI, S::BJ)) % kIndexCache];
-  };
-  auto issue_all = [&](int s) {
+  auto issue_b = [&](int n, int s, uint32_t to, auto tail_) {
+    constexpr bool tail = decltype(tail_)::value != 0;
+    const int u = n * S::W + wave;
+    const bool past = tail && s * kStepK + (KB ? kchunk : krow(u, S::BJ)) >= klen;
+    const char* const base = bbase + s * bstep;
     if constexpr (RowsB) {
+      const int row = src[n];  // -1 past the end
+      lds_load16(to + u * 1024, row < 0 ? zero : bbase + (int64_t)row * g.ldb * 2 + offb[n]);
+    } else if constexpr (!tail) {
+      lds_load16_at(to + u * 1024, base, offb[n]);
+    } else {
+      lds_load16(to + u * 1024, past ? zero : base + offb[n]);
+    }
+  };
+  // REG: load n of step s, waiting in registers for its stage.
+  u32x4 rega[REG ? S::LA : 1], regb[REG ? S::LB : 1];
+  auto fetch = [&](int s, auto la_) {
+    if constexpr (REG) {
+#pragma unroll
+      for (int n = 0; n < decltype(la_)::value; ++n) {
+        const int u = n * S::W + wave;
+        const char* p = abase + s * astep + offa[n];
+        int have;  // elements of the chunk
+        if constexpr (KA) {
+          have = klen - s * kStepK - kchunk;
+          if constexpr (RowsA) {
+            p = rowp[n] + s * astep;
+            if (!rowp[n]) have = 0;
+          }
+        } else {
+          const int k = krow(u, S::BI), c = lane % (S::BI / 8);
+          have = s * kStepK + k < klen ? ni - (((c >> 1) ^ unit_swizzle<S::BI>(k)) * 16 + (c & 1) * 8) : 0;
+        }
+        rega[n] = load8(reinterpret_cast<const uint16_t*>(p), have);
+      }
+#pragma unroll
+      for (int n = 0; n < S::LB; ++n) {
+        const int u = n * S::W + wave;
+        const char* p = bbase + s * bstep + offb[n];
+        int have;
+        if constexpr (KB) {
+          have = klen - s * kStepK - kchunk;
+        } else {
+          const int k = krow(u, S::BJ), c = lane % (S::BJ / 8);
+          have = s * kStepK + k < klen ? g.J - j0 - (((c >> 1) ^ unit_swizzle<S::BJ>(k)) * 16 + (c & 1) * 8) : 0;
+          if constexpr (RowsB) {
+            if (src[n] < 0) have = 0;
+            p = bbase + (int64_t)src[n] * g.ldb * 2 + offb[n];
+          }
+        }
+        regb[n] = load8(reinterpret_cast<const uint16_t*>(p), have);
+      }
+    }
+  };
+  auto put = [&](uint32_t sa, uint32_t sb, auto la_) {  // into the stages at sa, sb
+    if constexpr (REG) {
+#pragma unroll
+      for (int n = 0; n < decltype(la_)::value; ++n)
+        *reinterpret_cast<lds_u32x4*>(lds0 + sa + (n * S::W + wave) * 1024 + lane * 16) = rega[n];
+#pragma unroll
+      for (int n = 0; n < S::LB; ++n)
+        *reinterpret_cast<lds_u32x4*>(lds0 + 2 * S::StageA + sb + (n * S::W + wave) * 1024 + lane * 16) = regb[n];
+    }
+  };
+  // Gathered sums: the rows of step s.  A block of row indexes is put into LDS
+  // every kIndexCache rows.
+  auto next_rows = [&](int s) {
+    if constexpr (RowsB) {
+      int32_t* const index_cache = reinterpret_cast<int32_t*>(smem + S::Lds);
       if (s * kStepK % kIndexCache == 0) {
         __syncthreads();  // the last block's entries are read
-        fetch_indexes(s);
+        for (int i = threadIdx.x; i < kIndexCache; i += S::Threads) {
+          const int k = s * kStepK + i;
+          index_cache[i] = k < klen ? source_row(g, row0 + k0 + k) : -1;
+        }
+        __syncthreads();
       }
-      next_rows(s);
-    }
 #pragma unroll
-    for (int n = 0; n < S::LPW; ++n) issue(n, s);
+      for (int n = 0; n < S::LB; ++n)
+        src[n] = index_cache[(s * kStepK + krow(n * S::W + wave, S::BJ)) % kIndexCache];
+    }
   };
 
-  // ---- this wave's fragments
+  // ---- this wave's fragments.  Ragged rows: the waves take row blocks of 16 in
+  // turn, so that the blocks of a tile's valid rows are spread over them.
   const int wi = wave % S::WI, wj = wave / S::WI, l16 = lane & 15, quad = lane >> 4;
-  uint32_t fa0, fb0;
-  if constexpr (KA)
-    fa0 = wi * S::FI * 1024 + l16 * 64 + ((quad ^ chunk_swizzle(l16)) << 4);
-  else {
-    const int r = quad * 8 + (l16 >> 2);
-    fa0 = r * S::BI * 2 + (((wi * S::FI) ^ unit_swizzle<S::BI>(r)) << 5) + (l16 & 3) * 8;
-  }
-  if constexpr (KB)
-    fb0 = S::BI * 64 + wj * S::FJ * 1024 + l16 * 64 + ((quad ^ chunk_swizzle(l16)) << 4);
-  else {
-    const int r = quad * 8 + (l16 >> 2);
-    fb0 = S::BI * 64 + r * S::BJ * 2 + (((wj * S::FJ) ^ unit_swizzle<S::BJ>(r)) << 5) + (l16 & 3) * 8;
-  }
-  fa0 += lds0;
-  fb0 += lds0;
-  auto read_a = [&](int f, uint32_t stage) {
-    if constexpr (KA) return lds_read16(fa0 + stage + f * 1024);
-    else return lds_read_turned<S::BI>((fa0 + stage) ^ (uint32_t)(f << 5));
+  const int tr = quad * 8 + (l16 >> 2);  // a lane's row of a turned block
+  const uint32_t chunk0 = (uint32_t)(quad ^ (l16 & 7)) << 4;
+  const uint32_t fa0 = lds0 + (KA ? (wi * 16 + l16) * 128 + chunk0
+                                  : tr * S::BI * 2 + (((wi * S::FI) ^ unit_swizzle<S::BI>(tr)) << 5) + (l16 & 3) * 8);
+  const uint32_t fb0 = lds0 + 2 * S::StageA +
+                       (KB ? (wj * S::FJ * 16 + l16) * 128 + chunk0
+                           : tr * S::BJ * 2 + (((wj * S::FJ) ^ unit_swizzle<S::BJ>(tr)) << 5) + (l16 & 3) * 8);
+  // fragment f of half h of a step; `stage`: bytes to its stage
+  auto read_a = [&](int f, int h, uint32_t stage) {
+    if constexpr (KA) return lds_read16((fa0 + stage) ^ (uint32_t)(h << 6), f * S::WI * 2048);
+    else return lds_read_turned<S::BI>((fa0 + stage) ^ (uint32_t)(f << 5), h * 32 * S::BI * 2);
   };
-  auto read_b = [&](int f, uint32_t stage) {
-    if constexpr (KB) return lds_read16(fb0 + stage + f * 1024);
-    else return lds_read_turned<S::BJ>((fb0 + stage) ^ (uint32_t)(f << 5));
+  auto read_b = [&](int f, int h, uint32_t stage) {
+    if constexpr (KB) return lds_read16((fb0 + stage) ^ (uint32_t)(h << 6), f * 2048);
+    else return lds_read_turned<S::BJ>((fb0 + stage) ^ (uint32_t)(f << 5), h * 32 * S::BJ * 2);
   };
 
   f32x4 acc[S::FJ][S::FI] = {};
   u32x4 ra[2][S::FI], rb[2][S::FJ];
 
-  // One step: when it starts, its fragments are in registers (`cur`) or on
-  // their way there.
-  auto step = [&](int t, auto cur_) {
-    constexpr int cur = decltype(cur_)::value, nxt = cur ^ 1;
-    // step t + 1 has landed in LDS everywhere, and every wave has read step t
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::ST - 2) * S::LPW) : "memory");
-    const uint32_t stage = (uint32_t)((t + 1) % S::ST) * S::Stage;
-    if constexpr (RowsB) issue_all(t + S::ST);
+  // The sum with the first FA row fragments of each wave, LA loads of A a wave.
+  auto sum = [&](auto fa_, auto la_) {
+    constexpr int FA = decltype(fa_)::value, LA = decltype(la_)::value, F = FA + S::FJ;
+    uint32_t sa = 0, sb = 0;  // bytes to the current step's stages
+    // One step; its first half is in registers when it starts, or on the way.
+    auto step = [&](int t, auto tail_) {
+      const uint32_t sa1 = sa ^ S::StageA, sb1 = sb == (S::SB - 1) * S::StageB ? 0 : sb + S::StageB;
 #pragma unroll
-    for (int j = 0; j < S::FJ; ++j) {
-      if constexpr (!RowsB)
+      for (int j = 0; j < S::FJ; ++j) {
 #pragma unroll
-        for (int n = j * S::LPW / S::FJ; n < (j + 1) * S::LPW / S::FJ; ++n) issue(n, t + S::ST);
-      constexpr int F = S::FI + S::FJ;
+        for (int f = j * F / S::FJ; f < (j + 1) * F / S::FJ; ++f) {
+          if (f < S::FJ) rb[1][f] = read_b(f, 1, sb);
+          else ra[1][f - S::FJ] = read_a(f - S::FJ, 1, sa);
+        }
 #pragma unroll
-      for (int f = j * F / S::FJ; f < (j + 1) * F / S::FJ; ++f) {
-        if (f < S::FJ) rb[nxt][f] = read_b(f, stage);
-        else ra[nxt][f - S::FJ] = read_a(f - S::FJ, stage);
+        for (int i = 0; i < FA; ++i) acc[j][i] = T::mfma(rb[0][j], ra[0][i], acc[j][i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      // step t + 1 has landed in LDS everywhere, and every wave has read step t:
+      // its stages are free
+      if constexpr (REG) {
+        put(sa1, sb1, la_);
+        __syncthreads();
+      } else {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::SB - 2) * S::LB) : "memory");
+      }
+      next_rows(t + S::SB);
+      fetch(t + 2, la_);
 #pragma unroll
-      for (int i = 0; i < S::FI; ++i) acc[j][i] = T::mfma(rb[cur][j], ra[cur][i], acc[j][i]);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < S::FJ; ++j) {
+        constexpr int L = REG ? 0 : LA + S::LB;
+#pragma unroll
+        for (int n = j * L / S::FJ; n < (j + 1) * L / S::FJ; ++n) {
+          if (n < LA) issue_a(n, t + 2, lds0 + sa, tail_);
+          else issue_b(n - LA, t + S::SB, lds0 + 2 * S::StageA + sb, tail_);
+        }
+#pragma unroll
+        for (int f = j * F / S::FJ; f < (j + 1) * F / S::FJ; ++f) {
+          if (f < S::FJ) rb[0][f] = read_b(f, 0, sb1);
+          else ra[0][f - S::FJ] = read_a(f - S::FJ, 0, sa1);
+        }
+#pragma unroll
+        for (int i = 0; i < FA; ++i) acc[j][i] = T::mfma(rb[1][j], ra[1][i], acc[j][i]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      sa = sa1;
+      sb = sb1;
+    };
+    if constexpr (REG) {
+      next_rows(0);
+      fetch(0, la_);
+      put(0, 0, la_);
+      next_rows(1);
+      fetch(1, la_);
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int s = 0; s < S::SB; ++s) {
+        if (s < 2)
+#pragma unroll
+          for (int n = 0; n < LA; ++n) issue_a(n, s, lds0 + s * S::StageA, IntC<1>{});
+        next_rows(s);
+#pragma unroll
+        for (int n = 0; n < S::LB; ++n) issue_b(n, s, lds0 + 2 * S::StageA + s * S::StageB, IntC<1>{});
+      }
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(LA + (S::SB - 1) * S::LB) : "memory");
     }
+#pragma unroll
+    for (int f = 0; f < S::FJ; ++f) rb[0][f] = read_b(f, 0, 0);
+#pragma unroll
+    for (int f = 0; f < FA; ++f) ra[0][f] = read_a(f, 0, 0);
+    int t = 0;
+    for (; t + S::SB < full; ++t) step(t, IntC<0>{});
+    for (; t < nsteps; ++t) step(t, IntC<1>{});
   };
-#pragma unroll
-  for (int s = 0; s < S::ST; ++s) issue_all(s);
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S::ST - 1) * S::LPW) : "memory");
-#pragma unroll
-  for (int f = 0; f < S::FJ; ++f) rb[0][f] = read_b(f, 0);
-#pragma unroll
-  for (int f = 0; f < S::FI; ++f) ra[0][f] = read_a(f, 0);
-  for (int t = 0; t < nsteps; t += 2) {  // an odd last step is followed by one of zeros
-    step(t, IntC<0>{});
-    step(t + 1, IntC<1>{});
+  // A tile with few valid rows does without the fragments of the others.
+  constexpr int FI = S::FI, LA = S::LA;
+  const int fa = ((ni + 15) / 16 + S::WI - 1) / S::WI;
+  if (!KA || fa > FI * 3 / 4) {
+    sum(IntC<FI>{}, IntC<LA>{});
+  } else if constexpr (KA && FI >= 8) {
+    if (fa > FI / 2) sum(IntC<FI * 3 / 4>{}, IntC<(LA * 3 + 3) / 4>{});
+    else if (fa > FI / 4) sum(IntC<FI / 2>{}, IntC<(LA + 1) / 2>{});
+    else sum(IntC<FI / 4>{}, IntC<(LA + 3) / 4>{});
+  } else if constexpr (KA) {
+    if (fa > FI / 2) sum(IntC<FI>{}, IntC<LA>{});
+    else sum(IntC<FI / 2>{}, IntC<(LA + 1) / 2>{});
   }
   // loads past the end still write zeros to LDS: they end here, and every wave
   // has read its last fragments
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
   // ---- results: through LDS, 64 columns at a time, so that 16 lanes store one
-  // row's 64 neighbouring columns.  B's fragments are the matrix instruction's
-  // A operand: a lane holds four neighbouring columns of one row.  Each wave
-  // uses its own part; the 16-byte chunk c of row r lies at c ^ (r % 16).
-  constexpr int JC = S::JC, CH = JC * 4, Rows = S::FI * 16, RowBytes = JC * 64;
-  static_assert(S::W * Rows * RowBytes <= S::ST * S::Stage && S::FJ % JC == 0, "the parts fit the stages");
+  // row's 64 neighbouring columns, whole lines.  B's fragments are the matrix
+  // instruction's A operand: a lane holds four neighbouring columns of one row.
+  // Each wave uses its own part; the 16-byte chunk c of row r lies at c ^ (r % CH).
+  // Stores follow each other without waiting (U rows a lane in flight): a weight
+  // gradient of few rows an expert is bound by them.
+  constexpr int JC = S::JC, IC = S::IC, CH = JC * 4, Rows = IC * 16, RowBytes = JC * 64, At = 64 / CH;
+  constexpr int U = Rows / At < 8 ? Rows / At : 8;
   const uint32_t own = lds0 + wave * Rows * RowBytes;
   void* const c = OP == kWgrad ? result_of(g, e) : g.c;
   const int64_t slice = g.splits > 1 ? (int64_t)blockIdx.y * (OP == kWgrad ? g.E : 1) + (OP == kWgrad ? e : 0) : 0;
   float* const part = g.splits > 1 ? g.part + (slice * g.I + i0) * g.J : nullptr;
 #pragma unroll
-  for (int y0 = 0; y0 < S::FJ; y0 += JC) {
+  for (int y0 = 0; y0 < S::FJ; y0 += JC)
 #pragma unroll
-    for (int y = 0; y < JC; ++y)
+    for (int x0 = 0; x0 < S::FI; x0 += IC) {
 #pragma unroll
-      for (int x = 0; x < S::FI; ++x)
-        *reinterpret_cast<lds_f32x4*>(own + (x * 16 + l16) * RowBytes + (((y * 4 + quad) ^ (l16 % CH)) << 4)) =
-            acc[y0 + y][x];
-    const int ch = lane % CH, j = j0 + (wj * S::FJ + y0) * 16 + ch * 4;
+      for (int y = 0; y < JC; ++y)
+#pragma unroll
+        for (int x = 0; x < IC; ++x)
+          *reinterpret_cast<lds_f32x4*>(own + (x * 16 + l16) * RowBytes + (((y * 4 + quad) ^ (l16 % CH)) << 4)) =
+              acc[y0 + y][x0 + x];
+      const int ch = lane % CH, j = j0 + (wj * S::FJ + y0) * 16 + ch * 4;
+      if (j >= g.J) continue;
+      auto place = [&](int r) {  // row r of the part: its row of the tile
+        return KA ? ((x0 + r / 16) * S::WI + wi) * 16 + r % 16 : (wi * S::FI + x0) * 16 + r;
+      };
+      auto value = [&](int r) {
+        return *reinterpret_cast<const lds_f32x4*>(own + r * RowBytes + ((ch ^ (r % CH)) << 4));
+      };
+      if (g.plain || part) {
+        const int64_t ld = part ? g.J : g.ldc;
+        const int type = part ? (int)kF32 : g.c_type;
+        char* const to = static_cast<char*>(part ? part : c) +
+                         ((part ? 0 : (int64_t)i0 * ld) + j) * (type == kF32 ? 4 : 2);
+        const bool four = part ? g.J % 4 == 0 : true;
 #pragma unroll 1
-    for (int r = lane / CH; r < Rows; r += 64 / CH) {
-      const int di = wi * Rows + r;
-      if (di >= ni || j >= g.J) continue;
-      const f32x4 v = *reinterpret_cast<const lds_f32x4*>(own + r * RowBytes + ((ch ^ (r % 16 % CH)) << 4));
-      if (!part) {
-        finish4(g, c, i0 + di, j, v);
-        continue;
-      }
+        for (int r0 = lane / CH; r0 < Rows; r0 += At * U) {
+          f32x4 v[U];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (j + k < g.J) part[(int64_t)di * g.J + j + k] = v[k];
+          for (int u = 0; u < U; ++u) v[u] = value(r0 + u * At);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int di = place(r0 + u * At);
+            if (di >= ni) continue;
+            if (four) {
+              store4_from_f32(to, di * ld, type, v[u]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (j + k < g.J) reinterpret_cast<float*>(to)[di * ld + k] = v[u][k];
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int r = lane / CH; r < Rows; r += At)
+          if (place(r) < ni) finish4(g, c, i0 + place(r), j, value(r));
+      }
     }
-  }
 }
 
-template <typename T, int OP, typename S>
+template <typename T, int OP, bool REG, typename S>
 void launch_shape(const ProductArgs& a, hipStream_t stream) {
   const int ct = (a.J + S::BJ - 1) / S::BJ;
   const int64_t rt = OP == kWgrad ? (int64_t)a.E * ((a.I + S::BI - 1) / S::BI) : row_tiles_most(a, S::BI);
   const dim3 grid((unsigned)((rt * ct + 7) / 8 * 8), (unsigned)a.splits);
   if (OP != kDgrad && a.rows)
-    hipLaunchKernelGGL((product_lds_kernel<T, OP, OP != kDgrad, S>), grid, dim3(S::Threads), 0, stream, a, ct);
+    hipLaunchKernelGGL((product_lds_kernel<T, OP, OP != kDgrad, REG, S>), grid, dim3(S::Threads), 0, stream, a, ct);
   else
-    hipLaunchKernelGGL((product_lds_kernel<T, OP, false, S>), grid, dim3(S::Threads), 0, stream, a, ct);
+    hipLaunchKernelGGL((product_lds_kernel<T, OP, false, REG, S>), grid, dim3(S::Threads), 0, stream, a, ct);
 }
 
-
-using Big = Shape<256, 256, 2, 4, 4, 2>;
-using Mid = Shape<128, 128, 2, 2, 4, 2>;
-using Low = Shape<64, 128, 1, 4, 4, 3>;
-enum { kBig, kMid, kLow };
-
-// The tile shape of a product.  Rates of the three at 4096^3 (bf16, forward /
-// dgrad / wgrad): Big 1161 / 1193 / 1218 TFLOP/s, Mid 848 / 940 / 993, Low 640 /
-// 756 / 806; so the larger where its tiles occupy most of the 256 CUs and the
-// experts' rows fill most of a tile.  With 32 rows an expert (48 experts, 2304 x
-// 5120) Low takes 264 / 241 us for forward / dgrad, Mid 276 / 244, Big 330 /
-// 289, while wgrad, bound by its writes, takes 589, 574 and 513.
-inline int product_shape(const ProductArgs& a, int op) {
-  const int64_t live = !a.offsets ? 1 : a.E < a.P ? a.E : a.P;
-  const int64_t groups = op == kWgrad ? a.E : live ? live : 1;   // experts with results
-  const int64_t rows = op == kWgrad ? a.I : (a.P + groups - 1) / groups;  // of one, on average
-  const auto tiles = [&](int bi, int bj) { return groups * ((rows + bi - 1) / bi) * ((a.J + bj - 1) / bj); };
-  constexpr int kBusy = 200;
-  if (rows > 128 && tiles(256, 256) >= kBusy) return kBig;
-  if (rows > 64 && tiles(128, 128) >= kBusy) return kMid;
-  return kLow;
+template <typename T, int OP, int SB>
+void launch_tiles(const ProductArgs& a, int shape, hipStream_t stream) {
+  switch (shape) {
+    case kBig: return launch_shape<T, OP, false, Shape<256, 256, 2, 4, SB, 2>>(a, stream);
+    case kMid: return launch_shape<T, OP, false, Shape<128, 128, 2, 2, SB, 2>>(a, stream);
+    case kLow: return launch_shape<T, OP, false, Shape<64, 128, 1, 4, 2, 3>>(a, stream);
+    default: return launch_shape<T, OP, true, Shape<64, 128, 1, 4, 2, 3>>(a, stream);
+  }
 }
 
 }  // namespace

@@ -2,24 +2,12 @@
 #include "product_lds.h"
 
 namespace moe_fp4 {
-namespace {
 
-template <typename T>
-void launch(const ProductArgs& a, hipStream_t stream) {
-  switch (product_shape(a, kWgrad)) {
-    case kBig: return launch_shape<T, kWgrad, Big>(a, stream);
-    case kMid: return launch_shape<T, kWgrad, Mid>(a, stream);
-    default: return launch_shape<T, kWgrad, Low>(a, stream);
-  }
-}
-
-}  // namespace
-
-void launch_product_wgrad(const ProductArgs& a, hipStream_t stream) {
+void launch_product_wgrad(const ProductArgs& a, int shape, hipStream_t stream) {
   if (a.type == kBf16)
-    launch<Bf16>(a, stream);
+    launch_tiles<Bf16, kWgrad, 2>(a, shape, stream);
   else
-    launch<F16>(a, stream);
+    launch_tiles<F16, kWgrad, 2>(a, shape, stream);
 }
 
 }  // namespace moe_fp4

@@ -66,6 +66,13 @@ SHAPES = [  # counts, N, K
     ([0] * 100 + [17] + [0] * 100, 64, 128),
     ([1, 0, 2, 0, 1, 1, 0, 1], 576, 1280),
     ([513, 700], 264, 520),
+    # each tile shape at its own sizes: the largest, ragged; the middle one; and long sums in parts
+    ([700, 0, 1300, 257, 900, 64, 33, 1], 1032, 136),
+    ([130] * 9, 1032, 1160),
+    ([40, 0, 90], 64, 2048),
+    ([40, 33], 65, 2051),
+    ([3000, 5, 0, 2900], 72, 80),
+    ([2500, 1700], 35, 51),
 ]
 IDS = [f"E{len(c)}_P{sum(c)}_N{n}_K{k}" for c, n, k in SHAPES]
 

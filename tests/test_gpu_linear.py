@@ -53,7 +53,8 @@ SUBN = 2.0 ** -100
 
 SHAPES = [(1, 16, 32), (1, 1, 1), (1, 5120, 512), (1, 640, 5120), (2, 288, 320), (6, 512, 1024), (16, 100, 96),
           (17, 72, 2304), (33, 130, 77), (64, 256, 512), (100, 1001, 515), (129, 127, 130), (257, 264, 264),
-          (300, 512, 256), (5, 33, 1001), (1, 1001, 515), (700, 64, 64)]
+          (300, 512, 256), (5, 33, 1001), (1, 1001, 515), (700, 64, 64), (4, 999, 2051), (31, 257, 1029), (1300, 2064, 72),
+          (2000, 4104, 136), (48, 72, 5120), (40, 67, 4099)]
 
 
 @pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
@@ -143,7 +144,8 @@ def backward64(dy, x, w, z, act, dt):
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", [(1, 16, 32), (1, 1, 1), (3, 288, 320), (64, 256, 512), (100, 101, 115),
-                                   (300, 520, 264), (1030, 64, 96), (4100, 40, 24)])
+                                   (300, 520, 264), (1030, 64, 96), (4100, 40, 24), (4100, 33, 25), (600, 2056, 1544),
+                                   (5, 4096, 64)])
 def test_backward(moe, M, N, K, dt, act):
     g = gen(M * 11 + N + K)
     x, w = randn(g, M, K, dtype=dt), randn(g, N, K, dtype=dt, scale=K ** -0.5)
