@@ -39,34 +39,50 @@ struct F32 {
   static constexpr int kType = kF32;
 };
 
-// Element i of an array of a type known at run time (uniform over the grid).
-__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int type) {
-  if (type == kF32) return static_cast<const float*>(p)[i];
-  const uint16_t v = static_cast<const uint16_t*>(p)[i];
-  return type == kBf16 ? Bf16::to_f32(v) : F16::to_f32(v);
-}
-__device__ __forceinline__ void store_from_f32(void* p, int64_t i, int type, float v) {
-  if (type == kF32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<uint16_t*>(p)[i] = type == kBf16 ? Bf16::from_f32(v) : F16::from_f32(v);
-}
-
-// Activations in fp32.  gelu(z) = z Phi(z) with Phi from erfc, which keeps its
-// relative accuracy where Phi is small; the tanh form is z sigmoid(2 u) with
-// u = sqrt(2/pi) (z + 0.044715 z^3), which is 0.5 z (1 + tanh u) without its
-// cancellation.
-constexpr float kRsqrt2 = 0.70710678118654752f, kRsqrt2Pi = 0.39894228040143268f;
+// Activations in fp32, within a few steps of it: exp and the reciprocal are the
+// hardware's (one step each), an exponent's rounding adds about |exponent| half
+// steps.
+//
+// The tanh form of gelu is z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3): 0.5 z
+// (1 + tanh u) without its cancellation.  The exact form needs the normal
+// distribution Phi(z) = 1 - Phi(-z) and, for the slope, its density, which share
+// q = exp(-z^2 / 2): Phi(-u) = q R(u) for u >= 0 with R(u) = exp(u^2/2)
+// erfc(u / sqrt 2) / 2, a smooth function fitted as a polynomial of degree 8 in
+// t = 1 / (1 + 0.3 u) (least largest relative error, 5.8e-8, for u <= 14.5, past
+// which Phi(-u) is below fp32).  No cancellation on the small side; 2e-6
+// relative up to u = 6, 8e-6 up to 13.
+constexpr float kLog2e = 1.4426950408889634f, kRsqrt2Pi = 0.39894228040143268f;
 constexpr float kSqrt2OverPi = 0.79788456080286536f, kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
+__device__ __forceinline__ float exp_f32(float v) { return __builtin_amdgcn_exp2f(v * kLog2e); }
+__device__ __forceinline__ float sigmoid_f32(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-v));
+}
+__device__ __forceinline__ float normal_cdf(float z, float& q) {
+  const float u = fabsf(z), t = __builtin_amdgcn_rcpf(1.0f + 0.3f * u);
+  q = exp_f32(-0.5f * (z * z));
+  float r = 0x1.3aa226p-5f;
+  r = r * t - 0x1.5abde0p-3f;
+  r = r * t + 0x1.d4e4aep-3f;
+  r = r * t - 0x1.3abc3ep-4f;
+  r = r * t + 0x1.246220p-3f;
+  r = r * t + 0x1.836c76p-4f;
+  r = r * t + 0x1.f37ce0p-4f;
+  r = r * t + 0x1.e96846p-4f;
+  r = r * t + 0x1.eec0b4p-18f;
+  const float low = q * r;
+  return z < 0.0f ? low : 1.0f - low;
+}
+__device__ __forceinline__ float gelu_tanh_gate(float z) {
+  return sigmoid_f32(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+}
 
 __device__ __forceinline__ float activate(float z, int act) {
+  float q;
   switch (act) {
     case kActRelu: return z < 0.0f ? 0.0f : z;  // NaN stays NaN
-    case kActGelu: return z * (0.5f * erfcf(-z * kRsqrt2));
-    case kActGeluTanh:
-      return z * sigmoid_f32(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+    case kActGelu: return z * normal_cdf(z, q);
+    case kActGeluTanh: return z * gelu_tanh_gate(z);
     case kActSilu: return z * sigmoid_f32(z);
     default: return z;
   }
@@ -74,9 +90,13 @@ __device__ __forceinline__ float activate(float z, int act) {
 __device__ __forceinline__ float activate_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // 0 at 0; NaN stays NaN
-    case kActGelu: return 0.5f * erfcf(-z * kRsqrt2) + z * (kRsqrt2Pi * expf(-0.5f * z * z));
+    case kActGelu: {
+      float q;
+      const float p = normal_cdf(z, q);
+      return p + z * (kRsqrt2Pi * q);
+    }
     case kActGeluTanh: {
-      const float p = sigmoid_f32(2.0f * kSqrt2OverPi * (z + kGeluCubic * z * z * z));
+      const float p = gelu_tanh_gate(z);
       return p + z * (p * (1.0f - p)) * (2.0f * kSqrt2OverPi * (1.0f + 3.0f * kGeluCubic * z * z));
     }
     case kActSilu: {
@@ -160,15 +180,44 @@ typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
   if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
   u32x4 o = zero4();
+  if (n > 0) {  // all loads before the first use: one wait
+    uint32_t v[7];
 #pragma unroll
-  for (int i = 0; i < 7; ++i)
-    if (i < n) o[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+    for (int i = 0; i < 7; ++i) v[i] = p[i < n ? i : 0];
+#pragma unroll
+    for (int i = 0; i < 7; ++i) o[i / 2] |= i < n ? v[i] << (16 * (i & 1)) : 0u;
+  }
   return o;
 }
 
 // All eight, of data read once (weights): the caches keep it at low priority.
 __device__ __forceinline__ u32x4 load8_once(const uint16_t* p) {
   return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+}
+
+// Eight elements of type T (F32, Bf16 or F16) at any element's address as fp32,
+// those from n on as zeros.
+template <typename T>
+__device__ __forceinline__ void load8_as_f32(const void* p, int64_t i, int n, float (&v)[8]) {
+  if constexpr (T::kType == kF32) {
+    typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+    const float* const q = static_cast<const float*>(p) + i;
+    if (n >= 8) {
+      const f32x4 a = *reinterpret_cast<const f32x4_any*>(q), b = *reinterpret_cast<const f32x4_any*>(q + 4);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        v[r] = a[r];
+        v[4 + r] = b[r];
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) v[r] = r < n ? q[r] : 0.f;
+    }
+  } else {
+    const u32x4 a = load8(static_cast<const uint16_t*>(p) + i, n);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v[r] = T::to_f32((uint16_t)(a[r / 2] >> (16 * (r & 1))));
+  }
 }
 
 // Row of x that row s of the ragged side reads, or -1 for a zero row.
@@ -180,62 +229,91 @@ __device__ __forceinline__ int source_row(const ProductArgs& g, int s) {
   return r < g.R ? r : -1;
 }
 
-// Four neighbouring elements at a multiple of four, of an aligned array.
-__device__ __forceinline__ f32x4 load4_as_f32(const void* p, int64_t i, int type) {
-  if (type == kF32) return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
-  const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  const uint16_t h[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
+// The elements i .. i + 3 of an array, of which n exist: at once where the array
+// allows it (`wide`), else one by one, all loads before the first use.
+__device__ __forceinline__ f32x4 load4_as_f32(const void* p, int64_t i, int n, int type, bool wide) {
   f32x4 o;
+  if (type == kF32) {
+    const float* const q = static_cast<const float*>(p) + i;
+    if (wide) return *reinterpret_cast<const f32x4*>(q);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) o[r] = q[r < n ? r : 0];
+    return o;
+  }
+  const uint16_t* const q = static_cast<const uint16_t*>(p) + i;
+  uint16_t h[4];
+  if (wide) {
+    const uint2 v = *reinterpret_cast<const uint2*>(q);
+    h[0] = (uint16_t)v.x, h[1] = (uint16_t)(v.x >> 16), h[2] = (uint16_t)v.y, h[3] = (uint16_t)(v.y >> 16);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) h[r] = q[r < n ? r : 0];
+  }
 #pragma unroll
   for (int r = 0; r < 4; ++r) o[r] = type == kBf16 ? Bf16::to_f32(h[r]) : F16::to_f32(h[r]);
   return o;
 }
-__device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int type, const f32x4& v) {
+__device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int n, int type, bool wide, const f32x4& v) {
   if (type == kF32) {
-    *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = v;
+    float* const q = static_cast<float*>(p) + i;
+    if (wide) {
+      *reinterpret_cast<f32x4*>(q) = v;
+      return;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r < n) q[r] = v[r];
     return;
   }
+  uint16_t* const q = static_cast<uint16_t*>(p) + i;
   uint32_t h[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) h[r] = type == kBf16 ? Bf16::from_f32(v[r]) : F16::from_f32(v[r]);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  if (wide) {
+    *reinterpret_cast<uint2*>(q) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (r < n) q[r] = (uint16_t)h[r];
 }
 
-// What a product does with the sums of one row's columns j .. j + N - 1: bias,
-// the kept pre-activation, activation, residual and accumulation in fp32, then
-// one rounding to the result's type.  The activation takes the sum itself, not
-// its rounded copy z.
-template <int N>
-__device__ __forceinline__ void finish_columns(const ProductArgs& g, void* c, int64_t i, int j,
-                                               const f32x4& sum) {
+// What a product does with the sums of the columns j .. j + 3 of U rows (none
+// where row[u] is negative; `most` columns at most): bias, the kept
+// pre-activation, activation, residual and accumulation in fp32, then one
+// rounding to the result's type.  The activation takes the sum itself, not its
+// rounded copy z.  The rows' reads go out together, before any store.
+template <int U>
+__device__ __forceinline__ void finish(const ProductArgs& g, void* c, const int64_t (&row)[U], int j, int most,
+                                       const f32x4 (&sum)[U]) {
+  const int n = g.J - j < most ? g.J - j : most;
+  const bool wide = g.wide && most == 4;
+  const f32x4 bias = g.bias ? load4_as_f32(g.bias, j, n, g.bias_type, wide) : f32x4{};
+  f32x4 more[U], old[U];
 #pragma unroll
-  for (int r = 0; r < N; ++r) {
-    if (j + r >= g.J) break;
-    float v = sum[r];
-    if (g.bias) v += load_as_f32(g.bias, j + r, g.bias_type);
-    if (g.z) store_from_f32(g.z, i * g.ldz + j + r, g.type, v);
-    v = activate(v, g.act);
-    if (g.residual) v += load_as_f32(g.residual, i * g.ldr + j + r, g.c_type);
-    if (g.accumulate) v += load_as_f32(c, i * g.ldc + j + r, g.c_type);
-    store_from_f32(c, i * g.ldc + j + r, g.c_type, v);
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = row[u];
+    more[u] = g.residual && i >= 0 ? load4_as_f32(g.residual, i * g.ldr + j, n, g.c_type, wide) : f32x4{};
+    old[u] = g.accumulate && i >= 0 ? load4_as_f32(c, i * g.ldc + j, n, g.c_type, wide) : f32x4{};
   }
-}
-// The same for four columns, in one access of each array where they allow it (g.wide).
-__device__ __forceinline__ void finish4(const ProductArgs& g, void* c, int64_t i, int j,
-                                        const f32x4& sum) {
-  if (g.wide) {
-    f32x4 v = sum;
-    if (g.bias) v += load4_as_f32(g.bias, j, g.bias_type);
-    if (g.z) store4_from_f32(g.z, i * g.ldz + j, g.type, v);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t i = row[u];
+    f32x4 v = sum[u];
+    if (g.bias) v += bias;
+    if (g.z && i >= 0) store4_from_f32(g.z, i * g.ldz + j, n, g.type, wide, v);
     if (g.act != kActNone)
 #pragma unroll
       for (int r = 0; r < 4; ++r) v[r] = activate(v[r], g.act);
-    if (g.residual) v += load4_as_f32(g.residual, i * g.ldr + j, g.c_type);
-    if (g.accumulate) v += load4_as_f32(c, i * g.ldc + j, g.c_type);
-    store4_from_f32(c, i * g.ldc + j, g.c_type, v);
-    return;
+    if (g.residual) v += more[u];
+    if (g.accumulate) v += old[u];
+    if (i >= 0) store4_from_f32(c, i * g.ldc + j, n, g.c_type, wide, v);
   }
-finish_columns<4>(g, c, i, j, sum);
+}
+__device__ __forceinline__ void finish1(const ProductArgs& g, void* c, int64_t i, int j, int most, const f32x4& sum) {
+  const int64_t row[1] = {i};
+  const f32x4 sums[1] = {sum};
+  finish<1>(g, c, row, j, most, sums);
 }
 __device__ __forceinline__ void* result_of(const ProductArgs& g, int e) {
   return static_cast<char*>(g.c) + (int64_t)e * g.c_stride * (g.c_type == kF32 ? 4 : 2);

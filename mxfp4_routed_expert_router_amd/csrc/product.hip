@@ -30,9 +30,9 @@ __global__ void __launch_bounds__(256) product_join_kernel(ProductArgs g, int ch
     }
   }
   if (OP == kWgrad)
-    finish4(g, result_of(g, (int)(i / g.I)), i % g.I, j, v);
+    finish1(g, result_of(g, (int)(i / g.I)), i % g.I, j, 4, v);
   else
-    finish4(g, g.c, i, j, v);
+    finish1(g, g.c, i, j, 4, v);
 }
 
 // Whether both operands' rows are 16-byte aligned and a multiple of 8 long.

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(NW * 64) product_few_kernel(ProductArgs g) {
 #pragma unroll
   for (int i = 1; i < NW; ++i) v += sums[i][lane];
   const int j = j0 + quad * 4;
-  if (l16 < nrows && j < g.J) finish4(g, g.c, row0 + l16, j, v);
+  if (l16 < nrows && j < g.J) finish1(g, g.c, row0 + l16, j, 4, v);
 }
 
 // Sixteen waves where the workgroups would leave CUs with one (N = 2304, K = 5120,

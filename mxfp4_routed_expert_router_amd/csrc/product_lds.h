@@ -59,6 +59,13 @@ __device__ __forceinline__ u32x4 lds_read_turned(uint32_t a, int off) {
   return u32x4{l.x, l.y, h.x, h.y};
 }
 
+// An address that is the same in all lanes, into scalar registers.
+__device__ __forceinline__ const char* uniform(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const char*>((uint64_t)hi << 32 | lo);
+}
+
 // BI x BJ results, WI x WJ waves, SB stages of B; OCC waves per SIMD.
 template <int BI_, int BJ_, int WI_, int WJ_, int SB_, int OCC_>
 struct Shape {
@@ -124,9 +131,9 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // offset.  Indexes past an edge read the last one's data: their results are
   // not stored.  Gathered rows have 64-bit addresses of their own.
   const int first = OP == kWgrad ? row0 + k0 : k0;
-  const char* const abase = reinterpret_cast<const char*>(
+  const char* const abase = uniform(
       KA ? g.a + (RowsA ? 0 : (int64_t)i0 * g.lda) + k0 : g.a + (int64_t)first * g.lda + i0);
-  const char* const bbase = reinterpret_cast<const char*>(
+  const char* const bbase = uniform(
       KB ? b + (int64_t)j0 * g.ldb + k0 : b + (RowsB ? 0 : (int64_t)first * g.ldb) + j0);
   const int64_t astep = KA ? kStepK * 2 : kStepK * 2 * g.lda, bstep = KB ? kStepK * 2 : kStepK * 2 * g.ldb;
   const char* const zero = reinterpret_cast<const char*>(zero_chunk);
@@ -424,19 +431,23 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
           for (int u = 0; u < U; ++u) {
             const int di = place(r0 + u * At);
             if (di >= ni) continue;
-            if (four) {
-              store4_from_f32(to, di * ld, type, v[u]);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (j + k < g.J) reinterpret_cast<float*>(to)[di * ld + k] = v[u][k];
-            }
+            store4_from_f32(to, di * ld, g.J - j, type, four, v[u]);
           }
         }
       } else {
+        constexpr int V = Rows / At < 4 ? Rows / At : 4;
 #pragma unroll 1
-        for (int r = lane / CH; r < Rows; r += At)
-          if (place(r) < ni) finish4(g, c, i0 + place(r), j, value(r));
+        for (int r0 = lane / CH; r0 < Rows; r0 += At * V) {
+          f32x4 v[V];
+          int64_t row[V];
+#pragma unroll
+          for (int u = 0; u < V; ++u) {
+            v[u] = value(r0 + u * At);
+            const int di = place(r0 + u * At);
+            row[u] = di < ni ? i0 + di : -1;
+          }
+          finish<V>(g, c, row, j, 4, v);
+        }
       }
     }
 }

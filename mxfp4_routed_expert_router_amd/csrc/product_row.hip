@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(256) product_row_kernel(ProductArgs g) {
       const float s = wave_sum_f32(acc[r][m]);
       if (lane == m) v[r] = s;
     }
-  if (lane < nrows) finish_columns<R>(g, g.c, row0 + lane, j0, v);
+  if (lane < nrows) finish1(g, g.c, row0 + lane, j0, R, v);
 }
 
 template <typename T, int M, int R, int U>
