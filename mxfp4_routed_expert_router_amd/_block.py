@@ -23,6 +23,7 @@ GROUPED_FORWARD, GROUPED_DGRAD, GROUPED_WGRAD = range(3)
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _HALF = (torch.bfloat16, torch.float16)
 _ANY = (torch.float32, torch.bfloat16, torch.float16)
+_FP32 = (torch.float32,)
 
 _I32, _I64, _P, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
 
@@ -126,6 +127,17 @@ def _out_type(dtype, like, name: str = "out_dtype"):
     return dtype
 
 
+def _allowed(dtype, like):
+    """The types of a given result: as asked, or `like` and fp32."""
+    return (like, torch.float32) if dtype is None else (dtype,)
+
+
+def _given(t, name: str, dtype, like, device, shape, asked: str = "out_dtype") -> int:
+    """The row stride of a result that the caller gave."""
+    _out_type(dtype, like, asked)
+    return _rows(t, name, _allowed(dtype, like), device, shape)
+
+
 def _workspace(fn, d, *args, workspace, device):
     """The call's workspace: the given one (checked by the library), or a new one."""
     n = _SZ()
@@ -201,8 +213,9 @@ def moe_fp4_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Ten
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
-        y = torch.empty((P, N), dtype=_out_type(out_dtype, x.dtype), device=dev)
-    ldy = _rows(y, "y", (_out_type(out_dtype, y.dtype if y.dtype == torch.float32 else x.dtype),), dev, (P, N))
+        y, ldy = torch.empty((P, N), dtype=_out_type(out_dtype, x.dtype), device=dev), 0
+    else:
+        ldy = _given(y, "y", out_dtype, x.dtype, dev, (P, N))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[x.dtype], _TYPES[y.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
         ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_FORWARD,
@@ -230,8 +243,9 @@ def moe_fp4_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tens
     if dx is None:
         if accumulate:
             raise ValueError("accumulate needs dx")
-        dx = torch.empty((P, K), dtype=_out_type(out_dtype, dy.dtype), device=dev)
-    ldx = _rows(dx, "dx", (_out_type(out_dtype, dx.dtype if dx.dtype == torch.float32 else dy.dtype),), dev, (P, K))
+        dx, ldx = torch.empty((P, K), dtype=_out_type(out_dtype, dy.dtype), device=dev), 0
+    else:
+        ldx = _given(dx, "dx", out_dtype, dy.dtype, dev, (P, K))
     d = GroupedDims(E, P, N, K, P, 1, _TYPES[dy.dtype], _TYPES[dx.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
         ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_DGRAD,
@@ -263,9 +277,9 @@ def moe_fp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     if dw is None:
         if accumulate:
             raise ValueError("accumulate needs dw")
-        dw = torch.empty((E, N, K), dtype=_out_type(out_dtype, dy.dtype), device=dev)
-    ldw, es = _experts(dw, "dw", (_out_type(out_dtype, dw.dtype if dw.dtype == torch.float32 else dy.dtype),),
-                       dev, (E, N, K))
+        dw, ldw, es = torch.empty((E, N, K), dtype=_out_type(out_dtype, dy.dtype), device=dev), 0, 0
+    else:
+        ldw, es = _experts(dw, "dw", _allowed(out_dtype, dy.dtype), dev, (E, N, K))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[dy.dtype], _TYPES[dw.dtype], ldx, ldw, ldy, es)
     with _on(dev) as stream:
         ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_WGRAD,
@@ -306,8 +320,9 @@ def moe_fp4_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     if y is None:
         if accumulate:
             raise ValueError("accumulate needs y")
-        y = torch.empty((M, N), dtype=_out_type(out_dtype, x.dtype), device=dev)
-    ldy = _rows(y, "y", (_out_type(out_dtype, y.dtype if y.dtype == torch.float32 else x.dtype),), dev, (M, N))
+        y, ldy = torch.empty((M, N), dtype=_out_type(out_dtype, x.dtype), device=dev), 0
+    else:
+        ldy = _given(y, "y", out_dtype, x.dtype, dev, (M, N))
     ldr = _rows(residual, "residual", (y.dtype,), dev, (M, N)) if residual is not None else 0
     if bias is not None:
         _rows(bias, "bias", _ANY, dev, (N,), 1)
@@ -359,16 +374,18 @@ def moe_fp4_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opti
     if need_dx:
         if dx is None:
             dx = torch.empty((M, K), dtype=dt, device=dev)
-        lddx = _rows(dx, "dx", (dt,), dev, (M, K))
+        else:
+            lddx = _rows(dx, "dx", (dt,), dev, (M, K))
     if need_dw:
         if dw is None:
             dw = torch.empty((N, K), dtype=_out_type(dw_dtype, dt, "dw_dtype"), device=dev)
-        lddw = _rows(dw, "dw", (_out_type(dw_dtype, dw.dtype if dw.dtype == torch.float32 else dt, "dw_dtype"),),
-                     dev, (N, K))
+        else:
+            lddw = _given(dw, "dw", dw_dtype, dt, dev, (N, K), "dw_dtype")
     if need_db:
         if db is None:
             db = torch.empty(N, dtype=torch.float32, device=dev)
-        _rows(db, "db", (torch.float32,), dev, (N,), 1)
+        else:
+            _rows(db, "db", _FP32, dev, (N,), 1)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
     t = _TYPES[dt]
     d = LinearDims(M, N, K, t, _TYPES[dy.dtype], t, t if dw is None else _TYPES[dw.dtype], act, ldx, ldw, ldy, 0, ldz,
@@ -411,16 +428,17 @@ def moe_fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Op
         dt = x.dtype if out_dtype is None else out_dtype
         if dt not in _norm_y_types(x):
             raise TypeError(f"out_dtype must be one of {_norm_y_types(x)}")
-        y = torch.empty((T, H), dtype=dt, device=dev)
-    elif out_dtype is not None and y.dtype != out_dtype:
-        raise TypeError("y and out_dtype disagree")
-    ldy = _rows(y, "y", _norm_y_types(x), dev, (T, H))
+        y, ldy = torch.empty((T, H), dtype=dt, device=dev), 0
+    else:
+        if out_dtype is not None and y.dtype != out_dtype:
+            raise TypeError("y and out_dtype disagree")
+        ldy = _rows(y, "y", _norm_y_types(x), dev, (T, H))
     wt = _norm_weight(beta, "beta", H, dev, _norm_weight(gamma, "gamma", H, dev)) or x.dtype
     mean = rstd = None
     if save_stats:
         rstd = torch.empty(T, dtype=torch.float32, device=dev)
         if kind == NORM_LAYER:
-            mean = torch.empty(T, dtype=torch.float32, device=dev)
+            mean = torch.empty_like(rstd)
     d = NormDims(T, H, _TYPES[x.dtype], _TYPES[y.dtype], _TYPES[wt], kind, eps, ldx, ldy)
     with _on(dev) as stream:
         _check(_lib.moe_fp4_norm(d, x.data_ptr(), _opt(gamma), _opt(beta), y.data_ptr(), _opt(mean),
@@ -454,9 +472,9 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
         need_dbeta = gamma is not None and kind == NORM_LAYER
     if not (need_dx or need_dgamma or need_dbeta):
         raise ValueError("nothing to compute")
-    _rows(rstd, "rstd", (torch.float32,), dev, (T,), 1)
+    _rows(rstd, "rstd", _FP32, dev, (T,), 1)
     if kind == NORM_LAYER:
-        _rows(mean, "mean", (torch.float32,), dev, (T,), 1)
+        _rows(mean, "mean", _FP32, dev, (T,), 1)
     else:
         mean = None
     if accumulate and ((need_dgamma and dgamma is None) or (need_dbeta and dbeta is None)):
@@ -465,15 +483,18 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
     if need_dx:
         if dx is None:
             dx = torch.empty((T, H), dtype=x.dtype, device=dev)
-        lddx = _rows(dx, "dx", (x.dtype,), dev, (T, H))
+        else:
+            lddx = _rows(dx, "dx", (x.dtype,), dev, (T, H))
     if need_dgamma:
         if dgamma is None:
             dgamma = torch.empty(H, dtype=torch.float32, device=dev)
-        _rows(dgamma, "dgamma", (torch.float32,), dev, (H,), 1)
+        else:
+            _rows(dgamma, "dgamma", _FP32, dev, (H,), 1)
     if need_dbeta:
         if dbeta is None:
             dbeta = torch.empty(H, dtype=torch.float32, device=dev)
-        _rows(dbeta, "dbeta", (torch.float32,), dev, (H,), 1)
+        else:
+            _rows(dbeta, "dbeta", _FP32, dev, (H,), 1)
     dx, dgamma, dbeta = dx if need_dx else None, dgamma if need_dgamma else None, dbeta if need_dbeta else None
     d = NormDims(T, H, _TYPES[x.dtype], _TYPES[dy.dtype], _TYPES[wt], kind, 0.0, ldx, ldy, lddx)
     with _on(dev) as stream:
