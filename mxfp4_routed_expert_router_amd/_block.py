@@ -446,9 +446,10 @@ def moe_fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Op
     return (y, mean, rstd) if save_stats else y
 
 
-def moe_fp4_norm_backward_workspace_size(T: int, H: int) -> int:
+def moe_fp4_norm_backward_workspace_size(T: int, H: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace of moe_fp4_norm_backward for x of type `dtype`."""
     n = _SZ()
-    _check(_lib.moe_fp4_norm_backward_workspace_size(NormDims(T, H), n),
+    _check(_lib.moe_fp4_norm_backward_workspace_size(NormDims(T, H, _TYPES[dtype], _TYPES[dtype], F32), n),
            "moe_fp4_norm_backward_workspace_size")
     return n.value
 

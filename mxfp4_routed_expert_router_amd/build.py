@@ -15,7 +15,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["api.hip", "route.hip", "router.hip", "decode.hip", "prefill.hip", "prefill_lds.hip", "mx8.hip", "shared.hip", "stack.hip",
            "api_block.hip", "product.hip", "product_fwd.hip", "product_dgrad.hip",
            "product_wgrad.hip", "product_few.hip", "product_row.hip",
-           "slope.hip", "norm.hip"]
+           "slope.hip", "norm.hip", "norm_backward.hip"]
 
 # Packed fp32 VALU ops are switched off for all device code (the host pass warns
 # that it does not know the feature; that is harmless).

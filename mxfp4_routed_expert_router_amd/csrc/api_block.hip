@@ -204,9 +204,7 @@ int norm_args(const moe_fp4_norm_dims* dims, NormArgs& a) {
   a.eps = d.eps;
   return MOE_FP4_OK;
 }
-size_t norm_part_bytes(const moe_fp4_norm_dims& d) {
-  return (size_t)norm_blocks(d.T, d.H) * 2 * d.H * 4;
-}
+size_t norm_part_bytes(const NormArgs& a) { return (size_t)norm_blocks(a) * 2 * a.H * 4; }
 
 }  // namespace
 
@@ -353,7 +351,7 @@ int moe_fp4_norm_backward_workspace_size(const moe_fp4_norm_dims* dims, size_t* 
   NormArgs a;
   const int rc = norm_args(dims, a);
   if (rc != MOE_FP4_OK) return rc;
-  *bytes = norm_part_bytes(*dims);
+  *bytes = norm_part_bytes(a);
   return MOE_FP4_OK;
 }
 
@@ -372,7 +370,7 @@ int moe_fp4_norm_backward(const moe_fp4_norm_dims* dims, const void* dy, const v
       !aligned(rstd, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4))
     return MOE_FP4_EALIGN;
   if (dgamma || dbeta) {
-    const int wrc = workspace_check(ws, ws_bytes, norm_part_bytes(*dims));
+    const int wrc = workspace_check(ws, ws_bytes, norm_part_bytes(a));
     if (wrc != MOE_FP4_OK) return wrc;
   }
   a.x = x;

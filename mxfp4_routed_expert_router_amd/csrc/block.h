@@ -99,9 +99,9 @@ struct NormArgs {
   void* dx;
   float *dgamma, *dbeta;
   int accumulate;          // dgamma +=, dbeta +=
-  float* part;             // [norm_blocks(T, H)][2][H]
+  float* part;             // [norm_blocks][2][H]
 };
-int norm_blocks(int T, int H);  // workgroups of the backward pass
+int norm_blocks(const NormArgs& a);  // workgroups of the backward pass
 hipError_t launch_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, hipStream_t stream);
 

@@ -315,6 +315,21 @@ __device__ __forceinline__ void finish1(const ProductArgs& g, void* c, int64_t i
   const f32x4 sums[1] = {sum};
   finish<1>(g, c, row, j, most, sums);
 }
+// Sum of every eighth of a column's `parts` values from the p0-th on, `width`
+// apart: eight loads in flight, added in order.
+__device__ __forceinline__ float column_sum(const float* part, int64_t width, int p0, int parts) {
+  float v = 0.f;
+  int p = p0;
+  for (; p + 56 < parts; p += 64) {
+    float a[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a[u] = part[(p + 8 * u) * width];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += a[u];
+  }
+  for (; p < parts; p += 8) v += part[p * width];
+  return v;
+}
 __device__ __forceinline__ void* result_of(const ProductArgs& g, int e) {
   return static_cast<char*>(g.c) + (int64_t)e * g.c_stride * (g.c_type == kF32 ? 4 : 2);
 }

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) slope_columns_kernel(const float* part, i
   const int col = blockIdx.x * 32 + (threadIdx.x & 31), p0 = threadIdx.x >> 5;
   float v = 0.f;
   if (col < N)
-    for (int p = p0; p < parts; p += 8) v += part[(int64_t)p * N + col];
+    v = column_sum(part + col, N, p0, parts);
   s[p0][threadIdx.x & 31] = v;
   __syncthreads();
   if (p0 || col >= N) return;
