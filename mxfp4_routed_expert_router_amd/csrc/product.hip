@@ -61,7 +61,7 @@ struct Plan {
 // The tile shape and the number of parts of the sum that come out fastest for J
 // columns, by these measurements (us for a step of 64 of the sum, bf16, K = 5120;
 // the forms differ by a few percent):
-//   Big 256 x 256   up to 128 workgroups 1.2, 256: 1.6, 512: 3.1, 768: 4.6
+//   Big 256 x 256   up to 180 workgroups 1.27, 256: 1.6, 512: 3.1, 768: 4.6
 //   Mid 128 x 128   up to 256: 0.6, 512: 1.0, 768: 1.45, 1024: 1.9
 //   Low 64 x 128    up to 256: 0.54, 512: 0.68, 768: 1.0, 1024: 1.37
 // So Big goes in rounds of one workgroup a CU, the others flow.  A ragged tile
@@ -97,7 +97,7 @@ Tiles best_tiles(const ProductArgs& a, int op, int J) {
       double step;
       if (s == kBig && !ragged) {
         const double whole = (double)(int64_t)rounds, rest = wgs - whole * at;
-        step = 1.6 * whole + (rest > 128 ? 1.6 : rest > 0 ? 1.2 : 0);
+        step = 1.6 * whole + (rest > 192 ? 1.6 : rest > 0 ? 1.27 : 0);
       } else {
         step = rounds > 1 ? rounds * h.us[h.occ - 1] : h.us[wgs <= 256 ? 0 : wgs <= 512 ? 1 : 2];
       }
