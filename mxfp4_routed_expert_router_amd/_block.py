@@ -74,7 +74,7 @@ def _rows(t, name: str, dtypes, device=None, shape=None, ndim: int = 2) -> int:
     st, sz = t.stride(), t.shape
     if sz[-1] > 1 and st[-1] != 1:
         raise ValueError(f"{name} must be contiguous along its last dimension")
-    if ndim == 1 or sz[-2] <= 1:
+    if sz[-2] <= 1:
         return 0
     if st[-2] < sz[-1]:
         raise ValueError(f"{name} has rows that overlap (stride {st[-2]} of {sz[-1]} elements)")
@@ -92,7 +92,16 @@ def _refuse(t, name, dtypes, device, shape, ndim):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.dim() != ndim:
         raise ValueError(f"{name} must be a {ndim}-d tensor")
+    if tuple(t.shape) == tuple(shape):
+        raise ValueError(f"{name} must be contiguous")
     raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _vector(t, name: str, n: int, dtypes, device):
+    """Checks a contiguous vector of n elements."""
+    if not (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.shape == (n,) and
+            t.is_contiguous()):
+        _refuse(t, name, dtypes, device, (n,), 1)
 
 
 def _experts(t: torch.Tensor, name: str, dtypes, device=None, shape=None):
@@ -155,24 +164,20 @@ def _workspace(fn, d, *args, workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-class _on:
-    """Launches go to the tensors' device whatever the current one is, on its
-    current stream."""
-    __slots__ = ("index", "before")
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device):
-        self.index = device.index
 
-    def __enter__(self):
-        now = torch._C._cuda_getDevice()
-        self.before = now if now != self.index else -1
-        if now != self.index:
-            torch.cuda.set_device(self.index)
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.before >= 0:
-            torch.cuda.set_device(self.before)
+def _call(fn, device, *args):
+    """Calls the library for tensors on `device`, on its current stream, whatever
+    the current device is."""
+    i = device.index
+    if _device() == i:
+        rc = fn(*args, _raw_stream(i))
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, _raw_stream(i))
+    if rc:
+        _check(rc, fn.__name__)
 
 
 def _opt(t):
@@ -217,13 +222,10 @@ def moe_fp4_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Ten
     else:
         ldy = _given(y, "y", out_dtype, x.dtype, dev, (P, N))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[x.dtype], _TYPES[y.dtype], ldx, ldw, ldy, es)
-    with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_FORWARD,
-                                   workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_forward(d, x.data_ptr(), w.data_ptr(),
-                                            offsets.data_ptr(), _opt(rows), y.data_ptr(),
-                                            ACCUMULATE if accumulate else 0, ws, nws, stream),
-               "moe_fp4_grouped_forward")
+    ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_FORWARD, workspace=workspace,
+                               device=dev)
+    _call(_lib.moe_fp4_grouped_forward, dev, d, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), _opt(rows),
+          y.data_ptr(), ACCUMULATE if accumulate else 0, ws, nws)
     return y
 
 
@@ -247,13 +249,9 @@ def moe_fp4_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tens
     else:
         ldx = _given(dx, "dx", out_dtype, dy.dtype, dev, (P, K))
     d = GroupedDims(E, P, N, K, P, 1, _TYPES[dy.dtype], _TYPES[dx.dtype], ldx, ldw, ldy, es)
-    with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_DGRAD,
-                                   workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_dgrad(d, dy.data_ptr(), w.data_ptr(),
-                                          offsets.data_ptr(), dx.data_ptr(),
-                                          ACCUMULATE if accumulate else 0, ws, nws, stream),
-               "moe_fp4_grouped_dgrad")
+    ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_DGRAD, workspace=workspace, device=dev)
+    _call(_lib.moe_fp4_grouped_dgrad, dev, d, dy.data_ptr(), w.data_ptr(), offsets.data_ptr(), dx.data_ptr(),
+          ACCUMULATE if accumulate else 0, ws, nws)
     return dx
 
 
@@ -281,13 +279,9 @@ def moe_fp4_grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tens
     else:
         ldw, es = _experts(dw, "dw", _allowed(out_dtype, dy.dtype), dev, (E, N, K))
     d = GroupedDims(E, P, N, K, x.shape[0], row_div, _TYPES[dy.dtype], _TYPES[dw.dtype], ldx, ldw, ldy, es)
-    with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_WGRAD,
-                                   workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_grouped_wgrad(d, dy.data_ptr(), x.data_ptr(),
-                                          offsets.data_ptr(), _opt(rows), dw.data_ptr(),
-                                          ACCUMULATE if accumulate else 0, ws, nws, stream),
-               "moe_fp4_grouped_wgrad")
+    ws, nws, keep = _workspace(_lib.moe_fp4_grouped_workspace_size, d, GROUPED_WGRAD, workspace=workspace, device=dev)
+    _call(_lib.moe_fp4_grouped_wgrad, dev, d, dy.data_ptr(), x.data_ptr(), offsets.data_ptr(), _opt(rows),
+          dw.data_ptr(), ACCUMULATE if accumulate else 0, ws, nws)
     return dw
 
 
@@ -325,16 +319,13 @@ def moe_fp4_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
         ldy = _given(y, "y", out_dtype, x.dtype, dev, (M, N))
     ldr = _rows(residual, "residual", (y.dtype,), dev, (M, N)) if residual is not None else 0
     if bias is not None:
-        _rows(bias, "bias", _ANY, dev, (N,), 1)
+        _vector(bias, "bias", N, _ANY, dev)
     z = torch.empty((M, N), dtype=x.dtype, device=dev) if save_z else None
     t = _TYPES[x.dtype]
     d = LinearDims(M, N, K, t, _TYPES[y.dtype], t if bias is None else _TYPES[bias.dtype], t, act, ldx, ldw, ldy, ldr)
-    with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 0, workspace=workspace,
-                                   device=dev)
-        _check(_lib.moe_fp4_linear(d, x.data_ptr(), w.data_ptr(), _opt(bias), _opt(residual),
-                                   y.data_ptr(), _opt(z), ACCUMULATE if accumulate else 0, ws, nws, stream),
-               "moe_fp4_linear")
+    ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 0, workspace=workspace, device=dev)
+    _call(_lib.moe_fp4_linear, dev, d, x.data_ptr(), w.data_ptr(), _opt(bias), _opt(residual), y.data_ptr(), _opt(z),
+          ACCUMULATE if accumulate else 0, ws, nws)
     return (y, z) if save_z else y
 
 
@@ -385,25 +376,18 @@ def moe_fp4_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opti
         if db is None:
             db = torch.empty(N, dtype=torch.float32, device=dev)
         else:
-            _rows(db, "db", _FP32, dev, (N,), 1)
+            _vector(db, "db", N, _FP32, dev)
     dx, dw, db = dx if need_dx else None, dw if need_dw else None, db if need_db else None
     t = _TYPES[dt]
     d = LinearDims(M, N, K, t, _TYPES[dy.dtype], t, t if dw is None else _TYPES[dw.dtype], act, ldx, ldw, ldy, 0, ldz,
                    lddx, lddw)
-    with _on(dev) as stream:
-        ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 1, workspace=workspace,
-                                   device=dev)
-        _check(_lib.moe_fp4_linear_backward(d, dy.data_ptr(), _opt(x), _opt(w), _opt(z), _opt(dx),
-                                            _opt(dw), _opt(db), ACCUMULATE if accumulate else 0, ws, nws, stream),
-               "moe_fp4_linear_backward")
+    ws, nws, keep = _workspace(_lib.moe_fp4_linear_workspace_size, d, 1, workspace=workspace, device=dev)
+    _call(_lib.moe_fp4_linear_backward, dev, d, dy.data_ptr(), _opt(x), _opt(w), _opt(z), _opt(dx), _opt(dw), _opt(db),
+          ACCUMULATE if accumulate else 0, ws, nws)
     return dx, dw, db
 
 
 # ---------------------------------------------------------------- norms
-def _norm_types(x, name="x"):
-    return _rows(x, name, _ANY), x.device
-
-
 def _norm_y_types(x):
     return _ANY if x.dtype == torch.float32 else (x.dtype,)
 
@@ -411,7 +395,7 @@ def _norm_y_types(x):
 def _norm_weight(w, name, H, dev, other=None):
     if w is None:
         return other
-    _rows(w, name, _ANY if other is None else (other,), dev, (H,), 1)
+    _vector(w, name, H, _ANY if other is None else (other,), dev)
     return w.dtype
 
 
@@ -422,7 +406,8 @@ def moe_fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Op
     (NORM_RMS).  x fp32, bf16 or fp16; y of x's type, or any of the three for
     fp32 x.  With save_stats returns (y, mean, rstd), both [T] fp32, mean None
     for the RMS kind."""
-    ldx, dev = _norm_types(x)
+    ldx = _rows(x, "x", _ANY)
+    dev = x.device
     T, H = x.shape
     if y is None:
         dt = x.dtype if out_dtype is None else out_dtype
@@ -440,9 +425,7 @@ def moe_fp4_norm(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Op
         if kind == NORM_LAYER:
             mean = torch.empty_like(rstd)
     d = NormDims(T, H, _TYPES[x.dtype], _TYPES[y.dtype], _TYPES[wt], kind, eps, ldx, ldy)
-    with _on(dev) as stream:
-        _check(_lib.moe_fp4_norm(d, x.data_ptr(), _opt(gamma), _opt(beta), y.data_ptr(), _opt(mean),
-                                 _opt(rstd), stream), "moe_fp4_norm")
+    _call(_lib.moe_fp4_norm, dev, d, x.data_ptr(), _opt(gamma), _opt(beta), y.data_ptr(), _opt(mean), _opt(rstd))
     return (y, mean, rstd) if save_stats else y
 
 
@@ -463,7 +446,8 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
     """(dx, dgamma [H] fp32, dbeta [H] fp32) of moe_fp4_norm, None where not
     needed; by default dgamma where gamma is given and dbeta with it for the
     layer kind.  dx may be dy.  accumulate adds to the given dgamma and dbeta."""
-    ldx, dev = _norm_types(x)
+    ldx = _rows(x, "x", _ANY)
+    dev = x.device
     T, H = x.shape
     ldy = _rows(dy, "dy", _norm_y_types(x), dev, (T, H))
     wt = _norm_weight(gamma, "gamma", H, dev) or x.dtype
@@ -473,9 +457,9 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
         need_dbeta = gamma is not None and kind == NORM_LAYER
     if not (need_dx or need_dgamma or need_dbeta):
         raise ValueError("nothing to compute")
-    _rows(rstd, "rstd", _FP32, dev, (T,), 1)
+    _vector(rstd, "rstd", T, _FP32, dev)
     if kind == NORM_LAYER:
-        _rows(mean, "mean", _FP32, dev, (T,), 1)
+        _vector(mean, "mean", T, _FP32, dev)
     else:
         mean = None
     if accumulate and ((need_dgamma and dgamma is None) or (need_dbeta and dbeta is None)):
@@ -490,20 +474,17 @@ def moe_fp4_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[tor
         if dgamma is None:
             dgamma = torch.empty(H, dtype=torch.float32, device=dev)
         else:
-            _rows(dgamma, "dgamma", _FP32, dev, (H,), 1)
+            _vector(dgamma, "dgamma", H, _FP32, dev)
     if need_dbeta:
         if dbeta is None:
             dbeta = torch.empty(H, dtype=torch.float32, device=dev)
         else:
-            _rows(dbeta, "dbeta", _FP32, dev, (H,), 1)
+            _vector(dbeta, "dbeta", H, _FP32, dev)
     dx, dgamma, dbeta = dx if need_dx else None, dgamma if need_dgamma else None, dbeta if need_dbeta else None
     d = NormDims(T, H, _TYPES[x.dtype], _TYPES[dy.dtype], _TYPES[wt], kind, 0.0, ldx, ldy, lddx)
-    with _on(dev) as stream:
-        ws, nws, keep = None, 0, None
-        if need_dgamma or need_dbeta:
-            ws, nws, keep = _workspace(_lib.moe_fp4_norm_backward_workspace_size, d,
-                                       workspace=workspace, device=dev)
-        _check(_lib.moe_fp4_norm_backward(d, dy.data_ptr(), x.data_ptr(), _opt(gamma), _opt(mean),
-                                          rstd.data_ptr(), _opt(dx), _opt(dgamma), _opt(dbeta),
-                                          ACCUMULATE if accumulate else 0, ws, nws, stream), "moe_fp4_norm_backward")
+    ws, nws, keep = None, 0, None
+    if need_dgamma or need_dbeta:
+        ws, nws, keep = _workspace(_lib.moe_fp4_norm_backward_workspace_size, d, workspace=workspace, device=dev)
+    _call(_lib.moe_fp4_norm_backward, dev, d, dy.data_ptr(), x.data_ptr(), _opt(gamma), _opt(mean), rstd.data_ptr(),
+          _opt(dx), _opt(dgamma), _opt(dbeta), ACCUMULATE if accumulate else 0, ws, nws)
     return dx, dgamma, dbeta
