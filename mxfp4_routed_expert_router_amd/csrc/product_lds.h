@@ -390,14 +390,24 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // row's 64 neighbouring columns, whole lines.  B's fragments are the matrix
   // instruction's A operand: a lane holds four neighbouring columns of one row.
   // Each wave uses its own part; the 16-byte chunk c of row r lies at c ^ (r % CH).
-  // Stores follow each other without waiting (U rows a lane in flight): a weight
-  // gradient of few rows an expert is bound by them.
-  constexpr int JC = S::JC, IC = S::IC, CH = JC * 4, Rows = IC * 16, RowBytes = JC * 64, At = 64 / CH;
-  constexpr int U = Rows / At < 8 ? Rows / At : 8;
+  // Plain results leave as a scalar address, a lane's 32-bit offset and nothing to
+  // compute in between: a weight gradient of few rows an expert is bound by its
+  // stores (with addresses computed in each lane a 256 x 256 tile's end took 12700
+  // cycles, its start and one step 9000).
+  constexpr int JC = S::JC, IC = S::IC, CH = JC * 4, Rows = IC * 16, RowBytes = JC * 64, At = 64 / CH, Q = 16 / At;
   const uint32_t own = lds0 + wave * Rows * RowBytes;
   void* const c = OP == kWgrad ? result_of(g, e) : g.c;
   const int64_t slice = g.splits > 1 ? (int64_t)blockIdx.y * (OP == kWgrad ? g.E : 1) + (OP == kWgrad ? e : 0) : 0;
   float* const part = g.splits > 1 ? g.part + (slice * g.I + i0) * g.J : nullptr;
+  const int ch = lane % CH, lr = lane / CH;  // a lane's chunk and its first row of a part
+  // row r0 + lr of the wave's part at x0: r0 of the tile, in scalar registers
+  auto place = [&](int x0, int r0) {
+    return KA ? ((x0 + r0 / 16) * S::WI + wi) * 16 + r0 % 16 : (wi * S::FI + x0) * 16 + r0;
+  };
+  auto value = [&](int x, int q) {  // row 16 x + At q + lr of the part
+    return *reinterpret_cast<const lds_f32x4*>(
+        reinterpret_cast<lds_char*>(own + (q * At + lr) * RowBytes + ((ch ^ ((q * At + lr) % CH)) << 4)) + x * 16 * RowBytes);
+  };
 #pragma unroll
   for (int y0 = 0; y0 < S::FJ; y0 += JC)
 #pragma unroll
@@ -408,45 +418,49 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
         for (int x = 0; x < IC; ++x)
           *reinterpret_cast<lds_f32x4*>(own + (x * 16 + l16) * RowBytes + (((y * 4 + quad) ^ (l16 % CH)) << 4)) =
               acc[y0 + y][x0 + x];
-      const int ch = lane % CH, j = j0 + (wj * S::FJ + y0) * 16 + ch * 4;
+      const int jw = j0 + (wj * S::FJ + y0) * 16, j = jw + ch * 4;
       if (j >= g.J) continue;
-      auto place = [&](int r) {  // row r of the part: its row of the tile
-        return KA ? ((x0 + r / 16) * S::WI + wi) * 16 + r % 16 : (wi * S::FI + x0) * 16 + r;
-      };
-      auto value = [&](int r) {
-        return *reinterpret_cast<const lds_f32x4*>(own + r * RowBytes + ((ch ^ (r % CH)) << 4));
-      };
-      if (g.plain || part) {
+      if ((g.plain && !part) || (part && g.J % 4 == 0)) {
         const int64_t ld = part ? g.J : g.ldc;
-        const int type = part ? (int)kF32 : g.c_type;
-        char* const to = static_cast<char*>(part ? part : c) +
-                         ((part ? 0 : (int64_t)i0 * ld) + j) * (type == kF32 ? 4 : 2);
-        const bool four = part ? g.J % 4 == 0 : true;
-#pragma unroll 1
-        for (int r0 = lane / CH; r0 < Rows; r0 += At * U) {
-          f32x4 v[U];
+        const int type = part ? (int)kF32 : g.c_type, size = type == kF32 ? 4 : 2;
+        const char* const to = part ? reinterpret_cast<const char*>(part) + (int64_t)jw * 4
+                                    : static_cast<const char*>(c) + ((int64_t)i0 * ld + jw) * size;
+        const uint32_t lane_off = (uint32_t)(lr * ld + ch * 4) * size;
 #pragma unroll
-          for (int u = 0; u < U; ++u) v[u] = value(r0 + u * At);
+        for (int x = 0; x < IC; ++x)
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int di = place(r0 + u * At);
-            if (di >= ni) continue;
-            store4_from_f32(to, di * ld, g.J - j, type, four, v[u]);
+          for (int q = 0; q < Q; ++q) {
+            const int di = place(x0, x * 16 + q * At);
+            if (di + lr >= ni) continue;
+            char* const p = const_cast<char*>(uniform(to + di * ld * size)) + lane_off;
+            const f32x4 v = value(x, q);
+            if (type == kF32) {
+              *reinterpret_cast<f32x4*>(p) = v;
+            } else {
+              uint32_t h[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) h[r] = T::from_f32(v[r]);  // 16-bit results are of the operands' type
+              *reinterpret_cast<uint2*>(p) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            }
           }
-        }
       } else {
-        constexpr int V = Rows / At < 4 ? Rows / At : 4;
 #pragma unroll 1
-        for (int r0 = lane / CH; r0 < Rows; r0 += At * V) {
-          f32x4 v[V];
-          int64_t row[V];
+        for (int x = 0; x < IC; ++x) {
+          f32x4 v[Q];
+          int64_t row[Q];
 #pragma unroll
-          for (int u = 0; u < V; ++u) {
-            v[u] = value(r0 + u * At);
-            const int di = place(r0 + u * At);
-            row[u] = di < ni ? i0 + di : -1;
+          for (int q = 0; q < Q; ++q) {
+            v[q] = value(x, q);
+            const int di = place(x0, x * 16 + q * At) + lr;
+            row[q] = di < ni ? i0 + di : -1;
           }
-          finish<V>(g, c, row, j, 4, v);
+          if (!part) {
+            finish<Q>(g, c, row, j, 4, v);
+          } else {
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+              if (row[q] >= 0) store4_from_f32(part, (row[q] - i0) * g.J + j, g.J - j, kF32, false, v[q]);
+          }
         }
       }
     }
