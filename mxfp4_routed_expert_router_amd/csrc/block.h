@@ -48,7 +48,8 @@ struct ProductArgs {
   // [I][J] (wgrad [E][I][J]); 1: none
   int splits;
   float* part;
-  // set by launch_product: the epilogue takes four columns at a time; it only rounds
+  // set by launch_product: the epilogue takes four columns at a time; it only
+  // rounds and stores 16 bytes at a time
   int wide, plain;
 };
 

@@ -51,14 +51,23 @@ struct Chunk {
     }
   }
 };
-template <typename T>
+// kPast: the store passes the L2 (non-temporal).  It pays where a row is read and
+// written once: 16384 x 5120 bf16 forward 70.5 -> 67.6 us, x 2304 36.6 -> 29.5.  In
+// the backward pass it does not: f32 rows of 4096 147 -> 158 us.
+template <typename T, bool kPast>
 __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (T::kType == kF32) {
     typedef f32x4 __attribute__((aligned(4))) f32x4_word;
     float* const q = static_cast<float*>(p) + i;
     if (n >= 8) {
-      *reinterpret_cast<f32x4_word*>(q) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_word*>(q + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      const f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+      if constexpr (kPast) {
+        __builtin_nontemporal_store(a, reinterpret_cast<f32x4_word*>(q));
+        __builtin_nontemporal_store(b, reinterpret_cast<f32x4_word*>(q + 4));
+      } else {
+        *reinterpret_cast<f32x4_word*>(q) = a;
+        *reinterpret_cast<f32x4_word*>(q + 4) = b;
+      }
     } else {
 #pragma unroll
       for (int r = 0; r < 8; ++r)
@@ -71,7 +80,8 @@ __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const flo
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         o[r] = (uint32_t)T::from_f32(v[2 * r]) | ((uint32_t)T::from_f32(v[2 * r + 1]) << 16);
-      *reinterpret_cast<u32x4_any*>(q) = o;
+      if constexpr (kPast) __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(q));
+      else *reinterpret_cast<u32x4_any*>(q) = o;
     } else {
 #pragma unroll
       for (int r = 0; r < 8; ++r)

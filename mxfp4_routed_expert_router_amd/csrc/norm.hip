@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) norm_kernel(NormArgs g) {
     load_weight(g.beta, g.w_type, 8 * k, size(k), 0.0f, b);
 #pragma unroll
     for (int r = 0; r < 8; ++r) w[r] = x[c][r] * rstd * w[r] + b[r];
-    store_chunk<TY>(g.y, row * g.ldy + 8 * k, size(k), w);
+    store_chunk<TY, true>(g.y, row * g.ldy + 8 * k, size(k), w);
   }
 }
 

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(Threads) norm_backward_kernel(NormArgs g) {
         float o[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r) o[r] = rs * (d[c][r] - mg - x[c][r] * mgx);
-        store_chunk<TX>(g.dx, row * g.lddx + 8 * k, size(k), o);
+        store_chunk<TX, false>(g.dx, row * g.lddx + 8 * k, size(k), o);
       }
   }
   if (!g.part) return;
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(Threads) norm_backward_kernel(NormArgs g) {
 #pragma unroll
       for (int c = 0; c < CH; ++c)
         if (lt + c * TPR < nc)
-          store_chunk<F32>(part, which * g.H + (lt + c * TPR) * 8, size(lt + c * TPR), which ? db[c] : dw[c]);
+          store_chunk<F32, false>(part, which * g.H + (lt + c * TPR) * 8, size(lt + c * TPR), which ? db[c] : dw[c]);
     }
   }
 }

@@ -202,7 +202,9 @@ hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream) {
   };
   a.wide = a.J % 4 == 0 && four(a.c, a.ldc, a.c_type) && a.c_stride % 4 == 0 &&
            four(a.bias, 0, a.bias_type) && four(a.residual, a.ldr, a.c_type) && four(a.z, a.ldz, a.type);
-  a.plain = a.wide && !a.bias && !a.residual && !a.z && !a.accumulate && a.act == kActNone;
+  a.plain = a.wide && !a.bias && !a.residual && !a.z && !a.accumulate && a.act == kActNone &&
+            (a.c_type == kF32 || ((reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && a.ldc % 8 == 0 &&
+                                  a.c_stride % 8 == 0 && a.J % 8 == 0));
   a.part = static_cast<float*>(ws);
   a.splits = 1;
   const Plan p = plan(a, op);

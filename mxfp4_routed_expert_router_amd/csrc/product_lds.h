@@ -390,10 +390,13 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // row's 64 neighbouring columns, whole lines.  B's fragments are the matrix
   // instruction's A operand: a lane holds four neighbouring columns of one row.
   // Each wave uses its own part; the 16-byte chunk c of row r lies at c ^ (r % CH).
-  // Plain results leave as a scalar address, a lane's 32-bit offset and nothing to
-  // compute in between: a weight gradient of few rows an expert is bound by its
-  // stores (with addresses computed in each lane a 256 x 256 tile's end took 12700
-  // cycles, its start and one step 9000).
+  // Plain results leave 16 bytes a lane at a scalar address and a lane's 32-bit
+  // offset, four or eight rows' reads from LDS ahead of their stores: a weight
+  // gradient of few rows an expert is bound by this part.  They pass the L2 (non-
+  // temporal): other XCDs read them after the launch, whose end writes the L2
+  // back anyway, and 2.3 GB of weight gradients take 636 us against 776.  Parts of
+  // a split sum stay in it for the kernel that joins them (512 x 512 x 16384: 27.3
+  // us against 29.1).
   constexpr int JC = S::JC, IC = S::IC, CH = JC * 4, Rows = IC * 16, RowBytes = JC * 64, At = 64 / CH, Q = 16 / At;
   const uint32_t own = lds0 + wave * Rows * RowBytes;
   void* const c = OP == kWgrad ? result_of(g, e) : g.c;
@@ -419,31 +422,51 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
           *reinterpret_cast<lds_f32x4*>(own + (x * 16 + l16) * RowBytes + (((y * 4 + quad) ^ (l16 % CH)) << 4)) =
               acc[y0 + y][x0 + x];
       const int jw = j0 + (wj * S::FJ + y0) * 16, j = jw + ch * 4;
-      if (j >= g.J) continue;
-      if ((g.plain && !part) || (part && g.J % 4 == 0)) {
-        const int64_t ld = part ? g.J : g.ldc;
-        const int type = part ? (int)kF32 : g.c_type, size = type == kF32 ? 4 : 2;
-        const char* const to = part ? reinterpret_cast<const char*>(part) + (int64_t)jw * 4
-                                    : static_cast<const char*>(c) + ((int64_t)i0 * ld + jw) * size;
-        const uint32_t lane_off = (uint32_t)(lr * ld + ch * 4) * size;
+      // E columns a lane: a part's rows of the wave, read from LDS together, then
+      // stored; `all`: every row of the tile is valid; `past`: past the L2
+      auto leave = [&](auto e_, auto all_, auto past_, const char* to, int64_t ld) {
+        constexpr int E = decltype(e_)::value, Size = E == 8 ? 2 : 4, L = JC * 16 / E, A = 64 / L, N = 16 / A;
+        const int c0 = lane % L * (E / 4), r0 = lane / L;
+        if (jw + c0 * 4 >= g.J) return;
+        const uint32_t off = (uint32_t)(r0 * ld + c0 * 4) * Size;
 #pragma unroll
-        for (int x = 0; x < IC; ++x)
+        for (int x = 0; x < IC; ++x) {
+          f32x4 v[N][E / 4];
 #pragma unroll
-          for (int q = 0; q < Q; ++q) {
-            const int di = place(x0, x * 16 + q * At);
-            if (di + lr >= ni) continue;
-            char* const p = const_cast<char*>(uniform(to + di * ld * size)) + lane_off;
-            const f32x4 v = value(x, q);
-            if (type == kF32) {
-              *reinterpret_cast<f32x4*>(p) = v;
+          for (int q = 0; q < N; ++q)
+#pragma unroll
+            for (int h = 0; h < E / 4; ++h)
+              v[q][h] = *reinterpret_cast<const lds_f32x4*>(
+                  reinterpret_cast<lds_char*>(own + (q * A + r0) * RowBytes + (((c0 + h) ^ ((q * A + r0) % CH)) << 4)) +
+                  x * 16 * RowBytes);
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            const int di = place(x0, x * 16 + q * A);
+            if (!decltype(all_)::value && di + r0 >= ni) continue;
+            char* const p = const_cast<char*>(uniform(to + di * ld * Size)) + off;
+            if constexpr (E == 4) {
+              if constexpr (decltype(past_)::value) __builtin_nontemporal_store(v[q][0], reinterpret_cast<f32x4*>(p));
+              else *reinterpret_cast<f32x4*>(p) = v[q][0];
             } else {
-              uint32_t h[4];
+              u32x4 o;
 #pragma unroll
-              for (int r = 0; r < 4; ++r) h[r] = T::from_f32(v[r]);  // 16-bit results are of the operands' type
-              *reinterpret_cast<uint2*>(p) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+              for (int r = 0; r < 4; ++r)
+                o[r] = (uint32_t)T::from_f32(v[q][r / 2][r % 2 * 2]) |
+                       ((uint32_t)T::from_f32(v[q][r / 2][r % 2 * 2 + 1]) << 16);
+              __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
             }
           }
-      } else {
+        }
+      };
+      if (part && g.J % 4 == 0) {
+        leave(IntC<4>{}, IntC<0>{}, IntC<0>{}, reinterpret_cast<const char*>(part + jw), g.J);
+      } else if (g.plain && !part) {
+        const char* const to = static_cast<const char*>(c) + ((int64_t)i0 * g.ldc + jw) * (g.c_type == kF32 ? 4 : 2);
+        if (g.c_type == kF32)
+          ni == S::BI ? leave(IntC<4>{}, IntC<1>{}, IntC<1>{}, to, g.ldc) : leave(IntC<4>{}, IntC<0>{}, IntC<1>{}, to, g.ldc);
+        else  // of the operands' type
+          ni == S::BI ? leave(IntC<8>{}, IntC<1>{}, IntC<1>{}, to, g.ldc) : leave(IntC<8>{}, IntC<0>{}, IntC<1>{}, to, g.ldc);
+      } else if (j < g.J) {
 #pragma unroll 1
         for (int x = 0; x < IC; ++x) {
           f32x4 v[Q];
