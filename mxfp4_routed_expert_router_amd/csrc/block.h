@@ -48,9 +48,7 @@ struct ProductArgs {
   // [I][J] (wgrad [E][I][J]); 1: none
   int splits;
   float* part;
-  // set by launch_product: the epilogue takes four columns at a time; it only
-  // rounds and stores 16 bytes at a time
-  int wide, plain;
+  int plain;  // set by launch_product: the epilogue only rounds and stores, 16 bytes at a time
 };
 
 size_t product_workspace(const ProductArgs& a, int op);  // bytes of `part`

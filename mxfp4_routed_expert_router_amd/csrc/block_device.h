@@ -177,6 +177,7 @@ __device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, i
 // Eight elements at any element's address: p[0 .. n - 1], zeros behind (n <= 0:
 // nothing is read).  The hardware takes 16-byte loads at any address.
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_word;
 __device__ __forceinline__ u32x4 load8(const uint16_t* p, int n) {
   if (n >= 8) return *reinterpret_cast<const u32x4_any*>(p);
   u32x4 o = zero4();
@@ -200,10 +201,9 @@ __device__ __forceinline__ u32x4 load8_once(const uint16_t* p) {
 template <typename T>
 __device__ __forceinline__ void load8_as_f32(const void* p, int64_t i, int n, float (&v)[8]) {
   if constexpr (T::kType == kF32) {
-    typedef f32x4 __attribute__((aligned(4))) f32x4_any;
     const float* const q = static_cast<const float*>(p) + i;
     if (n >= 8) {
-      const f32x4 a = *reinterpret_cast<const f32x4_any*>(q), b = *reinterpret_cast<const f32x4_any*>(q + 4);
+      const f32x4 a = *reinterpret_cast<const f32x4_word*>(q), b = *reinterpret_cast<const f32x4_word*>(q + 4);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         v[r] = a[r];
@@ -229,13 +229,15 @@ __device__ __forceinline__ int source_row(const ProductArgs& g, int s) {
   return r < g.R ? r : -1;
 }
 
-// The elements i .. i + 3 of an array, of which n exist: at once where the array
-// allows it (`wide`), else one by one, all loads before the first use.
+// The elements i .. i + 3 of an array, at any element's address, of which n exist:
+// at once where all do (`wide`), else one by one, all loads before the first use.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 __device__ __forceinline__ f32x4 load4_as_f32(const void* p, int64_t i, int n, int type, bool wide) {
   f32x4 o;
   if (type == kF32) {
     const float* const q = static_cast<const float*>(p) + i;
-    if (wide) return *reinterpret_cast<const f32x4*>(q);
+    if (wide) return *reinterpret_cast<const f32x4_word*>(q);
 #pragma unroll
     for (int r = 0; r < 4; ++r) o[r] = q[r < n ? r : 0];
     return o;
@@ -243,8 +245,8 @@ __device__ __forceinline__ f32x4 load4_as_f32(const void* p, int64_t i, int n, i
   const uint16_t* const q = static_cast<const uint16_t*>(p) + i;
   uint16_t h[4];
   if (wide) {
-    const uint2 v = *reinterpret_cast<const uint2*>(q);
-    h[0] = (uint16_t)v.x, h[1] = (uint16_t)(v.x >> 16), h[2] = (uint16_t)v.y, h[3] = (uint16_t)(v.y >> 16);
+    const u32x2 v = *reinterpret_cast<const u32x2_any*>(q);
+    h[0] = (uint16_t)v[0], h[1] = (uint16_t)(v[0] >> 16), h[2] = (uint16_t)v[1], h[3] = (uint16_t)(v[1] >> 16);
   } else {
 #pragma unroll
     for (int r = 0; r < 4; ++r) h[r] = q[r < n ? r : 0];
@@ -257,7 +259,7 @@ __device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int n, int t
   if (type == kF32) {
     float* const q = static_cast<float*>(p) + i;
     if (wide) {
-      *reinterpret_cast<f32x4*>(q) = v;
+      *reinterpret_cast<f32x4_word*>(q) = v;
       return;
     }
 #pragma unroll
@@ -270,7 +272,7 @@ __device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int n, int t
 #pragma unroll
   for (int r = 0; r < 4; ++r) h[r] = type == kBf16 ? Bf16::from_f32(v[r]) : F16::from_f32(v[r]);
   if (wide) {
-    *reinterpret_cast<uint2*>(q) = uint2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+    *reinterpret_cast<u32x2_any*>(q) = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
     return;
   }
 #pragma unroll
@@ -287,7 +289,8 @@ template <int U>
 __device__ __forceinline__ void finish(const ProductArgs& g, void* c, const int64_t (&row)[U], int j, int most,
                                        const f32x4 (&sum)[U]) {
   const int n = g.J - j < most ? g.J - j : most;
-  const bool wide = g.wide && most == 4;
+  // of the whole wave, so that no condition stands between the reads
+  const bool wide = __builtin_amdgcn_ballot_w64(n != 4) == 0;
   const f32x4 bias = g.bias ? load4_as_f32(g.bias, j, n, g.bias_type, wide) : f32x4{};
   f32x4 more[U], old[U];
 #pragma unroll

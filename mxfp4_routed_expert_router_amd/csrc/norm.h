@@ -57,7 +57,6 @@ struct Chunk {
 template <typename T, bool kPast>
 __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (T::kType == kF32) {
-    typedef f32x4 __attribute__((aligned(4))) f32x4_word;
     float* const q = static_cast<float*>(p) + i;
     if (n >= 8) {
       const f32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};

@@ -21,8 +21,8 @@ __global__ void __launch_bounds__(256) product_join_kernel(ProductArgs g, int ch
   f32x4 v = {};
   for (int s = 0; s < g.splits; ++s) {
     const float* p = g.part + ((int64_t)s * rows + i) * g.J + j;
-    if (g.J % 4 == 0) {
-      v += *reinterpret_cast<const f32x4*>(p);
+    if (g.J - j >= 4) {
+      v += *reinterpret_cast<const f32x4_word*>(p);
     } else {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
@@ -197,14 +197,8 @@ size_t product_workspace(const ProductArgs& a, int op) {
 
 hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream) {
   if (op != kWgrad && a.P == 0) return hipSuccess;
-  const auto four = [](const void* p, int64_t ld, int type) {  // rows take 4 elements at once
-    return !p || ((reinterpret_cast<uintptr_t>(p) & (type == kF32 ? 15 : 7)) == 0 && ld % 4 == 0);
-  };
-  a.wide = a.J % 4 == 0 && four(a.c, a.ldc, a.c_type) && a.c_stride % 4 == 0 &&
-           four(a.bias, 0, a.bias_type) && four(a.residual, a.ldr, a.c_type) && four(a.z, a.ldz, a.type);
-  a.plain = a.wide && !a.bias && !a.residual && !a.z && !a.accumulate && a.act == kActNone &&
-            (a.c_type == kF32 || ((reinterpret_cast<uintptr_t>(a.c) & 15) == 0 && a.ldc % 8 == 0 &&
-                                  a.c_stride % 8 == 0 && a.J % 8 == 0));
+  a.plain = !a.bias && !a.residual && !a.z && !a.accumulate && a.act == kActNone &&
+            a.J % (a.c_type == kF32 ? 4 : 8) == 0;
   a.part = static_cast<float*>(ws);
   a.splits = 1;
   const Plan p = plan(a, op);

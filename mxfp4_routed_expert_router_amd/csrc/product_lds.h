@@ -202,62 +202,76 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
       lds_load16(to + u * 1024, past ? zero : base + offb[n]);
     }
   };
-  // REG: step s's loads, waiting in registers for their stage.  Forward loads its
-  // whole steps without a condition (2047 x 2303 x 5119 141 -> 138 us, 4000 x 333 x
-  // 2049 31 -> 29); the others, with edges along the columns too, gain nothing by it
-  // (wgrad of the latter 55 -> 58).
+  // REG: step s's loads, waiting in registers for their stage.  At an edge, where
+  // `have` of a chunk's eight elements are left, the eight that end there are read
+  // instead and moved down on their way to the stage: the loads of a step are under
+  // way together, behind no condition (gradients of 2047 x 2303 x 5119: rows 160 -> 117
+  // us, weights 194 -> 138; 333 x 1001 x 515: 33 -> 22, 18 -> 14).  Only rows
+  // of fewer than eight elements are read one by one.  Inlined by request: called,
+  // they would keep the registers in memory.
   u32x4 rega[REG ? S::LA : 1], regb[REG ? S::LB : 1];
-  auto fetch = [&](int s, auto la_, bool whole) {
+  const bool eight = (KA ? g.K : g.I) >= 8 && (KB ? g.K : g.J) >= 8;
+  auto left = [&](int n, int s, auto b_) __attribute__((always_inline)) {  // of load n of A or B
+    constexpr bool B = decltype(b_)::value != 0;
+    if constexpr (B ? KB : KA) {
+      return klen - s * kStepK - kchunk;
+    } else {
+      constexpr int BX = B ? S::BJ : S::BI;
+      const int k = krow(n * S::W + wave, BX), c = lane % (BX / 8);
+      return s * kStepK + k < klen ? (B ? g.J - j0 : ni) - (((c >> 1) ^ unit_swizzle<BX>(k)) * 16 + (c & 1) * 8) : 0;
+    }
+  };
+  auto fetch = [&](int s, auto la_) __attribute__((always_inline)) {
     if constexpr (REG) {
-      if (OP == kFwd && whole) {
+      auto from_a = [&](int n) { return RowsA ? rowp[RowsA ? n : 0] + s * astep : abase + s * astep + offa[n]; };
+      auto from_b = [&](int n) {
+        return RowsB ? bbase + (int64_t)src[RowsB ? n : 0] * g.ldb * 2 + offb[n] : bbase + s * bstep + offb[n];
+      };
+      auto have_a = [&](int n) { return RowsA && !rowp[RowsA ? n : 0] ? 0 : left(n, s, IntC<0>{}); };
+      auto have_b = [&](int n) { return RowsB && src[RowsB ? n : 0] < 0 ? 0 : left(n, s, IntC<1>{}); };
+      auto at = [&](const char* p, int have) {
+        return reinterpret_cast<const u32x4_any*>(have >= 8 ? p : have > 0 ? p - 2 * (8 - have) : zero);
+      };
+      if (OP == kFwd && s < full) {  // 2047 x 2303 x 5119: 138 us, 143 without
 #pragma unroll
-        for (int n = 0; n < decltype(la_)::value; ++n) {
-          const char* p = abase + s * astep + offa[n];
-          if constexpr (RowsA) p = rowp[n] ? rowp[n] + s * astep : zero;
-          rega[n] = *reinterpret_cast<const u32x4_any*>(p);
-        }
+        for (int n = 0; n < decltype(la_)::value; ++n)
+          rega[n] = *at(from_a(n), !RowsA || rowp[RowsA ? n : 0] ? 8 : 0);
 #pragma unroll
-        for (int n = 0; n < S::LB; ++n) regb[n] = *reinterpret_cast<const u32x4_any*>(bbase + s * bstep + offb[n]);
-        return;
-      }
+        for (int n = 0; n < S::LB; ++n) regb[n] = *at(from_b(n), 8);
+      } else if (eight) {
 #pragma unroll
-      for (int n = 0; n < decltype(la_)::value; ++n) {
-        const int u = n * S::W + wave;
-        const char* p = abase + s * astep + offa[n];
-        int have;  // elements of the chunk
-        if constexpr (KA) {
-          have = klen - s * kStepK - kchunk;
-          if constexpr (RowsA) {
-            p = rowp[n] + s * astep;
-            if (!rowp[n]) have = 0;
-          }
-        } else {
-          const int k = krow(u, S::BI), c = lane % (S::BI / 8);
-          have = s * kStepK + k < klen ? ni - (((c >> 1) ^ unit_swizzle<S::BI>(k)) * 16 + (c & 1) * 8) : 0;
-        }
-        rega[n] = load8(reinterpret_cast<const uint16_t*>(p), have);
-      }
+        for (int n = 0; n < decltype(la_)::value; ++n) rega[n] = *at(from_a(n), have_a(n));
 #pragma unroll
-      for (int n = 0; n < S::LB; ++n) {
-        const int u = n * S::W + wave;
-        const char* p = bbase + s * bstep + offb[n];
-        int have;
-        if constexpr (KB) {
-          have = klen - s * kStepK - kchunk;
-        } else {
-          const int k = krow(u, S::BJ), c = lane % (S::BJ / 8);
-          have = s * kStepK + k < klen ? g.J - j0 - (((c >> 1) ^ unit_swizzle<S::BJ>(k)) * 16 + (c & 1) * 8) : 0;
-          if constexpr (RowsB) {
-            if (src[n] < 0) have = 0;
-            p = bbase + (int64_t)src[n] * g.ldb * 2 + offb[n];
-          }
-        }
-        regb[n] = load8(reinterpret_cast<const uint16_t*>(p), have);
+        for (int n = 0; n < S::LB; ++n) regb[n] = *at(from_b(n), have_b(n));
+      } else {
+#pragma unroll
+        for (int n = 0; n < decltype(la_)::value; ++n)
+          rega[n] = load8(reinterpret_cast<const uint16_t*>(from_a(n)), have_a(n));
+#pragma unroll
+        for (int n = 0; n < S::LB; ++n) regb[n] = load8(reinterpret_cast<const uint16_t*>(from_b(n)), have_b(n));
       }
     }
   };
-  auto put = [&](uint32_t sa, uint32_t sb, auto la_) {  // into the stages at sa, sb
+  // step s, into the stages at sa, sb
+  auto put = [&](int s, uint32_t sa, uint32_t sb, auto la_) __attribute__((always_inline)) {
     if constexpr (REG) {
+      auto down = [&](u32x4& v, int have) __attribute__((always_inline)) {
+        const int back = have > 0 && have < 8 ? 8 - have : 0;
+        uint32_t w0 = v[0], w1 = v[1], w2 = v[2], w3 = v[3];
+        const bool four = back & 4, two = back & 2, one = back & 1;
+        w0 = four ? w2 : w0, w1 = four ? w3 : w1, w2 = four ? 0 : w2, w3 = four ? 0 : w3;
+        w0 = two ? w1 : w0, w1 = two ? w2 : w1, w2 = two ? w3 : w2, w3 = two ? 0 : w3;
+        const uint32_t sh = one ? 16 : 0;
+        v = u32x4{__builtin_amdgcn_alignbit(w1, w0, sh), __builtin_amdgcn_alignbit(w2, w1, sh),
+                  __builtin_amdgcn_alignbit(w3, w2, sh), w3 >> sh};
+      };
+      const bool whole = (s < full || !(KA || KB)) && (KA || ni == S::BI) && (KB || g.J - j0 >= S::BJ);
+      if (eight && !whole) {
+#pragma unroll
+        for (int n = 0; n < decltype(la_)::value; ++n) down(rega[n], left(n, s, IntC<0>{}));
+#pragma unroll
+        for (int n = 0; n < S::LB; ++n) down(regb[n], left(n, s, IntC<1>{}));
+      }
 #pragma unroll
       for (int n = 0; n < decltype(la_)::value; ++n)
         *reinterpret_cast<lds_u32x4*>(lds0 + sa + (n * S::W + wave) * 1024 + lane * 16) = rega[n];
@@ -329,13 +343,13 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
       // step t + 1 has landed in LDS everywhere, and every wave has read step t:
       // its stages are free
       if constexpr (REG) {
-        put(sa1, sb1, la_);
+        put(t + 1, sa1, sb1, la_);
         __syncthreads();
       } else {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S::SB - 2) * S::LB) : "memory");
       }
       next_rows(t + S::SB);
-      fetch(t + 2, la_, !decltype(tail_)::value);
+      fetch(t + 2, la_);
 #pragma unroll
       for (int j = 0; j < S::FJ; ++j) {
         constexpr int L = REG ? 0 : LA + S::LB;
@@ -358,10 +372,10 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
     };
     if constexpr (REG) {
       next_rows(0);
-      fetch(0, la_, full > 0);
-      put(0, 0, la_);
+      fetch(0, la_);
+      put(0, 0, 0, la_);
       next_rows(1);
-      fetch(1, la_, full > 1);
+      fetch(1, la_);
       __syncthreads();
     } else {
 #pragma unroll
@@ -380,7 +394,8 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
 #pragma unroll
     for (int f = 0; f < FA; ++f) ra[0][f] = read_a(f, 0, 0);
     int t = 0;
-    for (; t + S::SB < full; ++t) step(t, IntC<0>{});
+    if constexpr (!REG)
+      for (; t + S::SB < full; ++t) step(t, IntC<0>{});
     for (; t < nsteps; ++t) step(t, IntC<1>{});
   };
   // A tile with few valid rows does without the fragments of the others.
@@ -459,7 +474,7 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
             if (!decltype(all_)::value && di + r0 >= ni) continue;
             char* const p = const_cast<char*>(uniform(to + di * ld * Size)) + off;
             if constexpr (E == 4) {
-              if constexpr (decltype(past_)::value) __builtin_nontemporal_store(v[q][0], reinterpret_cast<f32x4*>(p));
+              if constexpr (decltype(past_)::value) __builtin_nontemporal_store(v[q][0], reinterpret_cast<f32x4_word*>(p));
               else *reinterpret_cast<f32x4*>(p) = v[q][0];
             } else {
               u32x4 o;
@@ -467,7 +482,7 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
               for (int r = 0; r < 4; ++r)
                 o[r] = (uint32_t)T::from_f32(v[q][r / 2][r % 2 * 2]) |
                        ((uint32_t)T::from_f32(v[q][r / 2][r % 2 * 2 + 1]) << 16);
-              __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(p));
+              __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(p));
             }
           }
         }
@@ -494,9 +509,10 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
           if (!part) {
             finish<Q>(g, c, row, j, 4, v);
           } else {
+            const bool wide = __builtin_amdgcn_ballot_w64(g.J - j < 4) == 0;
 #pragma unroll
             for (int q = 0; q < Q; ++q)
-              if (row[q] >= 0) store4_from_f32(part, (row[q] - i0) * g.J + j, g.J - j, kF32, false, v[q]);
+              if (row[q] >= 0) store4_from_f32(part, (row[q] - i0) * g.J + j, g.J - j, kF32, wide, v[q]);
           }
         }
       }
