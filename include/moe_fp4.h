@@ -340,7 +340,9 @@ int moe_fp4_quant_mxfp8(const uint16_t *src, int32_t rows, int32_t K, uint8_t *c
  *     start on 16-byte boundaries and are a multiple of 8 long run fastest.
  *   - Zero rows (P, M or T = 0) are allowed; arrays of no elements may be NULL.
  *   - Sums are fp32 in a fixed order: the same inputs give the same bits.  Each
- *     result is rounded once, to nearest, ties to even.
+ *     result is rounded once, to nearest, ties to even.  In a product, an fp16
+ *     input below 2^-14 keeps its value, but the additions' steps there are those
+ *     of 2^-14 (the matrix instruction aligns its terms by exponent field).
  *   - A workspace is sized by the operator's *_workspace_size, 256-byte
  *     aligned, needs no initialisation and may be NULL when its size is 0.  It
  *     belongs to one call at a time; two captured graphs that may replay at
