@@ -140,21 +140,16 @@ __device__ __forceinline__ int row_tiles(const int32_t* offsets, int E, int P, i
   return __builtin_amdgcn_readfirstlane(own);
 }
 
-// Row tile `t` of them: its expert, first row and row count.  False where t is
-// past the last one.
-__device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, int BM, int t,
-                                         int& e, int& row0, int& nrows) {
-  if (!offsets) {
-    e = 0;
-    row0 = t * BM;
-    nrows = P - row0 < BM ? P - row0 : BM;
-    return row0 < P;
-  }
+// The expert that owns row tile `t` of them, its first tile and its rows [lo,
+// lo + n).  False where t is past the last tile.
+__device__ __forceinline__ bool tile_owner(const int32_t* offsets, int E, int P, int BM, int t, int& e, int& first,
+                                           int& lo, int& n) {
   const int lane = threadIdx.x & 63;
+  int before = 0;  // tiles of the groups of experts passed
   for (int e0 = 0; e0 < E; e0 += 64) {
-    int lo = 0, n = 0;
-    if (e0 + lane < E) segment(offsets, e0 + lane, P, lo, n);
-    const int own = (n + BM - 1) / BM;
+    int l = 0, m = 0;
+    if (e0 + lane < E) segment(offsets, e0 + lane, P, l, m);
+    const int own = (m + BM - 1) / BM;
     int upto = own;  // tiles of this group's experts up to and with this lane's
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -162,18 +157,29 @@ __device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, i
       if (lane >= d) upto += o;
     }
     const int total = __builtin_amdgcn_readlane(upto, 63);
-    if (t < total) {
-      const int src = __ffsll((unsigned long long)__ballot(upto > t)) - 1;
-      const int first = __builtin_amdgcn_readlane(upto - own, src);
+    if (t - before < total) {
+      const int src = __ffsll((unsigned long long)__ballot(upto > t - before)) - 1;
       e = e0 + src;
-      row0 = __builtin_amdgcn_readlane(lo, src) + (t - first) * BM;
-      const int left = __builtin_amdgcn_readlane(n, src) - (t - first) * BM;
-      nrows = left < BM ? left : BM;
+      first = before + __builtin_amdgcn_readlane(upto - own, src);
+      lo = __builtin_amdgcn_readlane(l, src);
+      n = __builtin_amdgcn_readlane(m, src);
       return true;
     }
-    t -= total;
+    before += total;
   }
   return false;
+}
+
+// Row tile `t` of them: its expert, first row and row count.
+__device__ __forceinline__ bool row_tile(const int32_t* offsets, int E, int P, int BM, int t,
+                                         int& e, int& row0, int& nrows) {
+  int first = 0, lo = 0, n = P;
+  e = 0;
+  if (offsets && !tile_owner(offsets, E, P, BM, t, e, first, lo, n)) return false;
+  row0 = lo + (t - first) * BM;
+  const int left = n - (t - first) * BM;
+  nrows = left < BM ? left : BM;
+  return left > 0;
 }
 
 // Eight elements at any element's address: p[0 .. n - 1], zeros behind (n <= 0:

@@ -92,31 +92,35 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // ---- which tile: workgroups are dealt to the 8 XCDs round robin; each XCD
-  // takes a contiguous run of tiles, four row tiles of each column tile in turn,
-  // so that a run shares rows and weights in its L2
-  const int rt_all = OP == kWgrad ? g.E * ((g.I + S::BI - 1) / S::BI) : row_tiles(g.offsets, g.E, g.P, S::BI);
+  // takes a contiguous run of tiles, one expert's after another's, up to four row
+  // tiles of each column tile in turn, so that a run shares rows and weights in
+  // its L2
+  const int each = (g.I + S::BI - 1) / S::BI;  // row tiles of an expert's weights
+  const int rt_all = OP == kWgrad ? g.E * each : row_tiles(g.offsets, g.E, g.P, S::BI);
   const int64_t total = (int64_t)rt_all * col_tiles;
   const int64_t per = (total + 7) / 8, slot = blockIdx.x >> 3, tile = (blockIdx.x & 7) * per + slot;
   if (slot >= per || tile >= total) return;
-  constexpr int GR = 4;
-  const int band = (int)(tile / (GR * col_tiles)), in = (int)(tile - (int64_t)band * GR * col_tiles);
-  const int high = rt_all - band * GR < GR ? rt_all - band * GR : GR;
-  const int rt = band * GR + in % high, j0 = in / high * S::BJ;
-  int e, row0, nrows, i0, ni, klen;
-  const uint16_t* b = g.b;
+  int rt = (int)(tile / col_tiles), e = 0, first_tile = 0, lo = 0, rows = g.I;  // the tile's expert, and its rows
   if (OP == kWgrad) {
-    const int it = (g.I + S::BI - 1) / S::BI;
-    e = rt / it;
-    i0 = (rt - e * it) * S::BI;
-    ni = g.I - i0 < S::BI ? g.I - i0 : S::BI;
-    segment(g.offsets, e, g.P, row0, klen);
-  } else {
-    if (!row_tile(g.offsets, g.E, g.P, S::BI, rt, e, row0, nrows)) return;
-    i0 = row0;
-    ni = nrows;
-    klen = g.K;
-    b += (int64_t)e * g.w_stride;
+    e = rt / each;
+    first_tile = e * each;
+  } else if (g.offsets && !tile_owner(g.offsets, g.E, g.P, S::BI, rt, e, first_tile, lo, rows)) {
+    return;
   }
+  const int nt = (rows + S::BI - 1) / S::BI, bands = (nt + 3) / 4, high0 = (nt + bands - 1) / bands;
+  int64_t in = tile - (int64_t)first_tile * col_tiles;
+  const int band = (int)(in / ((int64_t)high0 * col_tiles)) * high0;  // its first row tile
+  in -= (int64_t)band * col_tiles;
+  const int high = nt - band < high0 ? nt - band : high0;
+  rt = band + (int)in % high;
+  const int j0 = (int)in / high * S::BJ, i0 = lo + rt * S::BI;
+  const int ni = rows - rt * S::BI < S::BI ? rows - rt * S::BI : S::BI;
+  int row0 = 0, klen = g.K;  // of the sum: wgrad's first row, and the length
+  const uint16_t* b = g.b;
+  if (OP == kWgrad)
+    segment(g.offsets, e, g.P, row0, klen);
+  else
+    b += (int64_t)e * g.w_stride;
   int k0 = 0;
   if (g.splits > 1) {
     const int share = ((klen + g.splits - 1) / g.splits + kStepK - 1) / kStepK * kStepK;
