@@ -61,17 +61,17 @@ struct Plan {
 // The tile shape and the number of parts of the sum that come out fastest for J
 // columns, by these measurements (us for a step of 64 of the sum, bf16, K = 5120;
 // the forms differ by a few percent):
-//   Big 256 x 256   up to 180 workgroups 1.27, 256: 1.6, 512: 3.1, 768: 4.6
-//   Mid 128 x 128   up to 256: 0.6, 512: 1.0, 768: 1.45, 1024: 1.9
-//   Low 64 x 128    up to 256: 0.54, 512: 0.68, 768: 1.0, 1024: 1.37
+//   Big 256 x 256   up to 180 workgroups 1.22, 256: 1.5, 512: 2.9, 768: 4.35
+//   Mid 128 x 128   up to 256: 0.55, 512: 0.94, 768: 1.37, 1024: 1.8
+//   Low 64 x 128    up to 256: 0.54, 512: 0.67, 768: 0.98, 1024: 1.32
 // So Big goes in rounds of one workgroup a CU, the others flow.  A ragged tile
 // with few rows takes less; the weights of all experts take their bytes' time
 // whatever the shape (48 experts of 2304 x 5120, 8, 32, 128 and 256 rows each:
-// Big 205, 209, 275, 391 us; Mid 201, 216, 297, 505; Low 226, 237, 386, 625).
+// Big 202, 205, 249, 360 us; Mid 200, 212, 309, 410; Low 228, 233, 332, 526).
 // Splitting the sum adds a launch and the parts' way to memory and back.
 Tiles best_tiles(const ProductArgs& a, int op, int J) {
   static const struct { int bi, bj, occ; double us[3], thin; } kShapes[3] = {
-      {256, 256, 1, {1.6, 1.6, 1.6}, 0.45}, {128, 128, 2, {0.6, 1.0, 1.0}, 0.5}, {64, 128, 3, {0.54, 0.68, 1.0}, 0.6}};
+      {256, 256, 1, {1.5, 1.5, 1.5}, 0.45}, {128, 128, 2, {0.55, 0.94, 0.94}, 0.5}, {64, 128, 3, {0.54, 0.67, 0.98}, 0.6}};
   const int64_t live = !a.offsets ? 1 : a.E < a.P ? a.E : a.P > 0 ? a.P : 1;
   const int64_t groups = op == kWgrad ? a.E : live;               // experts with results
   const double rows = op == kWgrad ? a.I : (double)a.P / groups;  // of one, on average
@@ -97,7 +97,7 @@ Tiles best_tiles(const ProductArgs& a, int op, int J) {
       double step;
       if (s == kBig && !ragged) {
         const double whole = (double)(int64_t)rounds, rest = wgs - whole * at;
-        step = 1.6 * whole + (rest > 192 ? 1.6 : rest > 0 ? 1.27 : 0);
+        step = 1.5 * whole + (rest > 192 ? 1.5 : rest > 0 ? 1.22 : 0);
       } else {
         step = rounds > 1 ? rounds * h.us[h.occ - 1] : h.us[wgs <= 256 ? 0 : wgs <= 512 ? 1 : 2];
       }
@@ -135,7 +135,7 @@ Plan plan(const ProductArgs& a, int op) {
     const int cut = (int)(rounds * 256 / rt) * 256;
     if (rounds >= 1 && cut > 0 && cut < a.J) {
       const Tiles rest = best_tiles(a, op, a.J - cut);
-      const double us = 1.6 * rounds * (double)((a.K + kSumStep - 1) / kSumStep + 3) + rest.us;
+      const double us = 1.5 * rounds * (double)((a.K + kSumStep - 1) / kSumStep + 3) + rest.us;
       if (us < p.main.us * 0.97) {
         p.main = {us, kBig, 1};
         p.rest = rest;
