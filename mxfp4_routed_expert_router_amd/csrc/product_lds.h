@@ -18,6 +18,11 @@
 // way to the registers: within 16 lanes, lane i receives column i of the four
 // rows that lanes 4 r .. 4 r + 3 address.  Its 32-byte units (16 indexes) of row
 // r sit at unit ^ unit_swizzle(r).
+//
+// Bound by the matrix cores and LDS together where the rows are many: 4096^3 bf16
+// 95 us forward, 97 rows' gradient, 102 weights' gradient (1.45, 1.42 and 1.35
+// PFLOP/s; a step of 256 x 256 takes 1.5 us).  By the weights' bytes where an expert
+// has few rows: 48 experts of 2304 x 5120, 32 rows each, 205 us (5.5 TB/s).
 #pragma once
 
 #include "block_device.h"
@@ -94,7 +99,8 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // ---- which tile: workgroups are dealt to the 8 XCDs round robin; each XCD
   // takes a contiguous run of tiles, one expert's after another's, up to four row
   // tiles of each column tile in turn, so that a run shares rows and weights in
-  // its L2
+  // its L2 (24576 rows on 64 experts 630 us; 667 with bands of four row tiles that
+  // pass an expert's end)
   const int each = (g.I + S::BI - 1) / S::BI;  // row tiles of an expert's weights
   const int rt_all = OP == kWgrad ? g.E * each : row_tiles(g.offsets, g.E, g.P, S::BI);
   const int64_t total = (int64_t)rt_all * col_tiles;
