@@ -89,9 +89,12 @@ __device__ __forceinline__ float activate(float z, int act) {
     default: return z;
   }
 }
+// The slopes are 1 and 0 in fp32 long before |z| = 1000.  There z is held, so that
+// no 0 * inf follows where z^2 passes fp32 or z is infinite (a kept fp16 z may be).
 __device__ __forceinline__ float activate_slope(float z, int act) {
+  if (act == kActRelu) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // 0 at 0; NaN stays NaN
+  z = fabsf(z) > 1000.0f ? copysignf(1000.0f, z) : z;
   switch (act) {
-    case kActRelu: return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;  // 0 at 0; NaN stays NaN
     case kActGelu: {
       float q;
       const float p = normal_cdf(z, q);
