@@ -440,8 +440,12 @@ int moe_fp4_linear(const moe_fp4_linear_dims *dims, const void *x, const void *w
 /* The gradients, with dz = dy * act'(z):
  *   dx = dz W (type)      dw = dz^T x (dw_type)      db[n] = sum_m dz[m][n] (fp32)
  * Each of dx, dw, db may be NULL (at least one is not).  x is read for dw, w
- * for dx, z where act is not NONE; they may be NULL otherwise.  dz is rounded
- * to `type` for the two products (not for db).  The residual's gradient is dy.
+ * for dx, z where act is not NONE; they may be NULL otherwise.  Where dz is not
+ * dy itself (an act, or dy in fp32), it is rounded to `type` for the two
+ * products (not for db).  In fp16 a common power of two keeps dz in range there,
+ * whatever dy's: it brings the largest finite |dz| into [2^14, 2^15), is taken
+ * back from the fp32 sums, and the rounding is off by 2^-11 of a value or 2^-39 of
+ * that largest |dz|, whichever is more.  The residual's gradient is dy.
  * flags: MOE_FP4_ACCUMULATE adds to dw and db (dx is always overwritten).
  * Errors: as moe_fp4_linear. */
 int moe_fp4_linear_backward(const moe_fp4_linear_dims *dims, const void *dy, const void *x,

@@ -150,6 +150,7 @@ ProductArgs linear_forward_args(const moe_fp4_linear_dims& d, const LinearStride
 }
 // dz is dy itself where nothing changes between them
 bool dz_is_dy(const moe_fp4_linear_dims& d) { return d.act == kActNone && d.out_type == d.type; }
+bool dz_has_factor(const moe_fp4_linear_dims& d) { return d.type == kF16 && !dz_is_dy(d); }
 ProductArgs linear_dgrad_args(const moe_fp4_linear_dims& d, const LinearStrides& s) {
   ProductArgs a = linear_product(d);
   a.I = d.M; a.J = d.K; a.K = d.N;
@@ -164,16 +165,21 @@ ProductArgs linear_wgrad_args(const moe_fp4_linear_dims& d, const LinearStrides&
   a.c_type = d.dw_type;
   return a;
 }
-// Workspace of the backward pass: dz, the column sums' parts, the products' parts
-// (the two run one after the other and share theirs).
+// Workspace of the backward pass: dz, its power of two in fp16 and the parts that it is
+// found from, the column sums' parts, the products' parts (the two run one after the
+// other and share theirs).
 struct BackwardWs {
-  size_t dz, part, product, total;
+  size_t dz, factor, top, part, product, total;
 };
 BackwardWs backward_layout(const moe_fp4_linear_dims& d, const LinearStrides& s) {
   BackwardWs w{};
   size_t o = 0;
   w.dz = o;
   if (!dz_is_dy(d)) o = align_up(o + (size_t)d.M * d.N * 2);
+  w.factor = o;
+  if (dz_has_factor(d)) o += kAlign;
+  w.top = o;
+  if (dz_has_factor(d)) o = align_up(o + kSlopeTops * 4);
   w.part = o;
   o = align_up(o + (size_t)slope_blocks(d.M) * d.N * 4);
   w.product = o;
@@ -295,6 +301,7 @@ int moe_fp4_linear_backward(const moe_fp4_linear_dims* dims, const void* dy, con
   const int acc = (flags & MOE_FP4_ACCUMULATE) ? 1 : 0;
   const bool direct = dz_is_dy(d);
   const uint16_t* dz = static_cast<const uint16_t*>(dy);
+  float* const factor = dz_has_factor(d) ? reinterpret_cast<float*>(base + l.factor) : nullptr;
   hipError_t err = hipSuccess;
   if (db || (!direct && (dx || dw))) {
     SlopeArgs p{};
@@ -304,6 +311,8 @@ int moe_fp4_linear_backward(const moe_fp4_linear_dims* dims, const void* dy, con
     if (!direct && (dx || dw)) {
       p.dz = reinterpret_cast<uint16_t*>(base + l.dz);
       dz = p.dz;
+      p.factor = factor;
+      p.top = reinterpret_cast<float*>(base + l.top);
     }
     p.db = db; p.accumulate = acc;
     p.part = reinterpret_cast<float*>(base + l.part);
@@ -314,6 +323,7 @@ int moe_fp4_linear_backward(const moe_fp4_linear_dims* dims, const void* dy, con
     a.a = dz;
     a.b = static_cast<const uint16_t*>(w);
     a.c = dx;
+    a.factor = factor;
     err = launch_product(a, kDgrad, base + l.product, stream);
   }
   if (err == hipSuccess && dw) {
@@ -321,6 +331,7 @@ int moe_fp4_linear_backward(const moe_fp4_linear_dims* dims, const void* dy, con
     a.a = dz;
     a.b = static_cast<const uint16_t*>(x);
     a.c = dw;
+    a.factor = factor;
     a.accumulate = acc;
     err = launch_product(a, kWgrad, base + l.product, stream);
   }

@@ -48,7 +48,8 @@ struct ProductArgs {
   // [I][J] (wgrad [E][I][J]); 1: none
   int splits;
   float* part;
-  int plain;  // set by launch_product: the epilogue only rounds and stores, 16 bytes at a time
+  const float* factor;  // of the sums, on the device, or null (1)
+  int plain;  // set by launch_product: the epilogue only multiplies by the factor, rounds and stores, 16 bytes at a time
 };
 
 size_t product_workspace(const ProductArgs& a, int op);  // bytes of `part`
@@ -69,7 +70,10 @@ inline int64_t row_tiles_most(const ProductArgs& a, int BM) {
   return (a.P + live * (BM - 1)) / BM;
 }
 
-// dz = dy act'(z) in `type`, and the column sums of dz before that rounding.
+// dz = dy act'(z) in `type`, and the column sums of dz before that rounding.  In
+// fp16, dz is multiplied by a power of two 2^s first, which the products of dz take
+// back by their factor 2^-s.
+constexpr int kSlopeTops = 1024;
 struct SlopeArgs {
   int M, N, type, dy_type, act;
   const void* dy;
@@ -80,9 +84,12 @@ struct SlopeArgs {
   float* db;           // [N] or null
   int accumulate;      // db +=
   float* part;         // [slope_blocks(M)][N], with db
+  float* top;          // [kSlopeTops], with dz in fp16: parts of the largest |dz|
+  int tops;            // set by launch_slope: how many parts
+  float* factor;       // with dz in fp16: written, 2^-s
 };
 int slope_blocks(int M);
-hipError_t launch_slope(const SlopeArgs& a, hipStream_t stream);
+hipError_t launch_slope(SlopeArgs a, hipStream_t stream);
 
 struct NormArgs {
   int T, H;

@@ -292,7 +292,7 @@ __device__ __forceinline__ void store4_from_f32(void* p, int64_t i, int n, int t
 }
 
 // What a product does with the sums of the columns j .. j + 3 of U rows (none
-// where row[u] is negative; `most` columns at most): bias, the kept
+// where row[u] is negative; `most` columns at most): the factor, bias, the kept
 // pre-activation, activation, residual and accumulation in fp32, then one
 // rounding to the result's type.  The activation takes the sum itself, not its
 // rounded copy z.  The rows' reads go out together, before any store.
@@ -303,6 +303,7 @@ __device__ __forceinline__ void finish(const ProductArgs& g, void* c, const int6
   // of the whole wave, so that no condition stands between the reads
   const bool wide = __builtin_amdgcn_ballot_w64(n != 4) == 0;
   const f32x4 bias = g.bias ? load4_as_f32(g.bias, j, n, g.bias_type, wide) : f32x4{};
+  const float factor = g.factor ? *g.factor : 1.0f;
   f32x4 more[U], old[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -314,6 +315,7 @@ __device__ __forceinline__ void finish(const ProductArgs& g, void* c, const int6
   for (int u = 0; u < U; ++u) {
     const int64_t i = row[u];
     f32x4 v = sum[u];
+    if (g.factor) v *= factor;
     if (g.bias) v += bias;
     if (g.z && i >= 0) store4_from_f32(g.z, i * g.ldz + j, n, g.type, wide, v);
     if (g.act != kActNone)

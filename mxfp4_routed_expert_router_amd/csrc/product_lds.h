@@ -441,6 +441,8 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   void* const c = OP == kWgrad ? result_of(g, e) : g.c;
   const int64_t slice = g.splits > 1 ? (int64_t)blockIdx.y * (OP == kWgrad ? g.E : 1) + (OP == kWgrad ? e : 0) : 0;
   float* const part = g.splits > 1 ? g.part + (slice * g.I + i0) * g.J : nullptr;
+  constexpr bool Factor = T::kType == kF16 && OP != kFwd;  // only a dense backward pass in fp16 has one
+  const float factor = Factor && g.factor ? *g.factor : 1.0f;
   const int ch = lane % CH, lr = lane / CH;  // a lane's chunk and its first row of a part
   // row r0 + lr of the wave's part at x0: r0 of the tile, in scalar registers
   auto place = [&](int x0, int r0) {
@@ -478,6 +480,11 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
               v[q][h] = *reinterpret_cast<const lds_f32x4*>(
                   reinterpret_cast<lds_char*>(own + (q * A + r0) * RowBytes + (((c0 + h) ^ ((q * A + r0) % CH)) << 4)) +
                   x * 16 * RowBytes);
+          if constexpr (Factor && decltype(past_)::value)
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+#pragma unroll
+              for (int h = 0; h < E / 4; ++h) v[q][h] *= factor;
 #pragma unroll
           for (int q = 0; q < N; ++q) {
             const int di = place(x0, x * 16 + q * A);

@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+from block_common import U32, bounded, gen, half_step, randn, slope64
+
 pytestmark = pytest.mark.gpu
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -50,3 +52,106 @@ def test_slope_of_nan_is_nan(moe, act):
     dx, _, db = moe.moe_fp4_linear_backward(dy, None, w, z=z, act=a, need_dw=False)
     assert torch.isnan(db).tolist() == [False] * 3 + [True] + [False] * 4
     assert torch.isnan(dx).all(1).tolist() == [False, True]
+
+
+def backward64(dy, x, w, z, act, top=None):
+    """dx, dw, db of fp16 operands in 64 bits, and bounds of each before its rounding.
+
+    dz = dy act'(z) is rounded to fp16 after a power of two that brings its largest
+    finite magnitude `top` into [2^14, 2^15): off by half a step of the value, or of the
+    smallest numbers of the type, 2^-25 after that power, at most 2^-39 top before it.
+    The products' additions keep steps of 2^-14 below it (terms are aligned by exponent
+    field): of 2^-28 top at most on the side of dz."""
+    M, N = dy.shape
+    if act == "none":
+        dz, e = dy, torch.zeros_like(dy)
+    else:
+        # the slope's evaluation; its terms cancel where it is small, so relative to 1 + |z|
+        dz = dy * slope64(z, act)
+        e = dy.abs() * (16 + 8 * z.abs()) * U32 * 1.2
+    e_db = e.sum(0) + (M + 1) * U32 * (dz.abs() + e).sum(0)
+    top = dz.abs().max() if top is None else top
+    e16 = e + torch.maximum(half_step(HF) * (dz.abs() + e), 2.0 ** -39 * top)
+    mag = torch.maximum(dz.abs() + e16, 2.0 ** -28 * top)
+    up = lambda v: v.abs().clamp(min=2.0 ** -14)
+    e_dx = e16 @ w.abs() + N * U32 * (mag @ up(w))
+    e_dw = e16.t() @ x.abs() + M * U32 * (mag.t() @ up(x))
+    return (dz @ w, dz.t() @ x, dz.sum(0)), (e_dx, e_dw, e_db)
+
+
+DZ_SHAPES = [(1, 16, 32), (3, 7, 5), (70, 96, 128), (100, 101, 115), (300, 520, 264), (4100, 33, 25), (5, 4096, 64),
+             (600, 2056, 1544)]
+
+
+@pytest.mark.parametrize("power", [-60, -30, -18, 0, 18, 60, "mixed"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu"])
+@pytest.mark.parametrize("M,N,K", DZ_SHAPES)
+def test_fp32_gradients_into_fp16_products(moe, M, N, K, act, power):
+    """dy in fp32 passes fp16's range at both ends; dw and db are fp32 and hold the answer."""
+    g = gen(M + N + K)
+    x, w, z = randn(g, M, K, dtype=HF), randn(g, N, K, dtype=HF, scale=2.0 ** -12), randn(g, M, N, dtype=HF)
+    dy = randn(g, M, N)
+    if power == "mixed":  # gradients of very different size next to each other
+        dy *= torch.exp2(torch.randint(-30, 19, (M, N), generator=g, device="cuda").float())
+    else:
+        dy *= 2.0 ** power
+    a = {"none": moe.ACT_NONE, "silu": moe.ACT_SILU, "gelu": moe.ACT_GELU}[act]
+    (wx, ww, wb), (ex, ew, eb) = backward64(dy.double(), x.double(), w.double(), z.double(), act)
+    holds = wx.abs().max().item() < 60000  # dx is fp16
+    dx, dw, db = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=a, dw_dtype=F32, need_dx=holds)
+    if holds:
+        bounded(dx, wx, ex, HF, "dx")
+    bounded(dw, ww, ew, F32, "dw")
+    bounded(db, wb, eb, F32, "db")
+    more = dw.clone()
+    moe.moe_fp4_linear_backward(dy, x, w, z=z, act=a, dw=more, need_dx=False, need_db=False, accumulate=True)
+    bounded(more, ww + dw.double(), ew + U32 * ww.abs(), F32, "dw +=")
+
+
+@pytest.mark.parametrize("power", [-22, 0])
+@pytest.mark.parametrize("M,N,K", DZ_SHAPES)
+def test_small_fp16_gradients(moe, M, N, K, power):
+    """dy in fp16 near its smallest numbers: the slope's digits are not lost."""
+    g = gen(M + N + K + 1)
+    x, w, z = randn(g, M, K, dtype=HF), randn(g, N, K, dtype=HF), randn(g, M, N, dtype=HF)
+    dy = (randn(g, M, N) * 2.0 ** power).to(HF)
+    (wx, ww, wb), (ex, ew, eb) = backward64(dy.double(), x.double(), w.double(), z.double(), "silu")
+    dx, dw, db = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=moe.ACT_SILU, dw_dtype=F32)
+    bounded(dx, wx, ex, HF, "dx")
+    bounded(dw, ww, ew, F32, "dw")
+    bounded(db, wb, eb, F32, "db")
+
+
+@pytest.mark.parametrize("dyt", [HF, F32], ids=["f16", "f32"])
+def test_an_infinite_gradient_stays_in_its_row(moe, dyt):
+    """The power of two goes by the finite values: the other rows keep theirs."""
+    g = gen(11)
+    M, N, K = 70, 96, 128
+    x, w, z = randn(g, M, K, dtype=HF), randn(g, N, K, dtype=HF), randn(g, M, N, dtype=HF)
+    dy = randn(g, M, N, dtype=dyt)
+    dy[7, 5], dy[20, 3], dy[21, 90] = float("inf"), float("nan"), float("-inf")
+    dx, _, db = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=moe.ACT_SILU)
+    ok = torch.isfinite(dy).all(1)
+    assert (~torch.isfinite(dx).all(1)).nonzero().flatten().tolist() == [7, 20, 21]
+    dz = dy.double() * slope64(z.double(), "silu")
+    top = dz[torch.isfinite(dz)].abs().max()
+    (wx, _, _), (ex, _, _) = backward64(dy[ok].double(), x[ok].double(), w.double(), z[ok].double(), "silu", top)
+    bounded(dx[ok], wx, ex, HF, "dx")
+    assert (~torch.isfinite(db)).nonzero().flatten().tolist() == [3, 5, 90]
+
+
+@pytest.mark.parametrize("value", [0.0, 1e-45, 3.4e38])
+def test_gradients_at_the_ends_of_fp32(moe, value):
+    g = gen(12)
+    M, N, K = 9, 8, 16
+    x, w = torch.ones(M, K, dtype=HF, device="cuda"), torch.ones(N, K, dtype=HF, device="cuda")
+    dy = torch.zeros(M, N, device="cuda")
+    dy[4, 2] = value
+    _, dw, db = moe.moe_fp4_linear_backward(dy, x, w, need_dx=False, dw_dtype=F32)
+    # one term each: 2^126 is the largest power, so the smallest fp32 numbers lie 2^-23
+    # below 1 there and fp16 keeps them to 2^-25
+    want = torch.zeros(N, K, dtype=torch.float64, device="cuda")
+    want[2] = dy[4, 2].double()
+    lim = half_step(HF) * want.abs() + 2.0 ** -151
+    assert bool(((dw.double() - want).abs() <= lim).all())
+    assert torch.equal(db, dy.sum(0))
