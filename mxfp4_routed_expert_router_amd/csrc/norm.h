@@ -6,9 +6,12 @@
 //   dgamma = sum_t dy xhat,  dbeta = sum_t dy
 //
 // Both passes are bound by memory: a row is read once into registers, its sums
-// are taken from there (the variance from the centred values, so a mean far
-// from zero costs no digits), and the result is written once.  All sums are
-// fp32 in a fixed order: the same inputs give the same bits.
+// are taken from there, and the result is written once.  The forward pass takes the
+// deviations from a first mean, and their own mean corrects them, the mean and the
+// variance: the first mean is off by a few steps of itself, up to 0.25 in a row
+// of 1e6, which would be all the deviation that a row of one value shows (y = 1
+// where it is 0).  16384 x 5120 bf16 takes 64.5 us with that, 63.8 without.  All
+// sums are fp32 in a fixed order: the same inputs give the same bits.
 #pragma once
 
 #include "block_device.h"

@@ -7,6 +7,7 @@ from block_common import U32, bounded, gen, half_step, randn, slope64
 pytestmark = pytest.mark.gpu
 
 BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+EPS = 1e-6
 
 
 @pytest.fixture(scope="module")
@@ -155,3 +156,48 @@ def test_gradients_at_the_ends_of_fp32(moe, value):
     lim = half_step(HF) * want.abs() + 2.0 ** -151
     assert bool(((dw.double() - want).abs() <= lim).all())
     assert torch.equal(db, dy.sum(0))
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (F32, BF), (BF, BF), (HF, HF)], ids=["f32", "f32_bf16", "bf16", "f16"])
+@pytest.mark.parametrize("H", [1, 7, 33, 200, 1000, 1024, 2304, 4095, 5120, 8192, 16383, 16384])
+def test_constant_rows_far_from_zero(moe, H, types):
+    """Rows of one value have no deviations, whatever the rounding of their sum: y = 0.
+
+    A row's sum passes at most n = 48 additions one after another (24 or fewer of a
+    thread, 6 of a wave, 16 waves, the product by 1 / H), so the first mean is off by
+    n U |c| and what the second step leaves of that by n U of it; the deviations are
+    divided by sqrt(eps) at least."""
+    xt, yt = types
+    values = [1000.1, -3.3, 123456.7, 1000000.3, -0.1, 7e-4]
+    if xt == HF:
+        values = [1000.1, -3.3, 65504.0, -0.1, 7e-4]
+    c = torch.tensor(values, device="cuda").to(xt)
+    x = c[:, None].expand(-1, H).contiguous()
+    y, mean, rstd = moe.moe_fp4_norm(x, eps=EPS, out_dtype=yt, save_stats=True)
+    c = c.double()
+    left = (48 * U32) ** 2 * c.abs()
+    assert bool((y.double().abs() <= 1.02 * left[:, None] / EPS ** 0.5 + 2.0 ** -25).all()), y.abs().max(1)
+    assert bool(((mean.double() - c).abs() <= U32 * c.abs() + left).all())
+    # the variance: the squares of the first deviations, n U |c| at most, cancel to n U of them
+    var = 50 * U32 * (48 * U32 * c) ** 2
+    want = EPS ** -0.5
+    near = var < 1e-3 * EPS
+    assert bool(((rstd.double() - want).abs() <= (0.51 * var / EPS + 8 * U32) * want)[near].all())
+
+
+@pytest.mark.parametrize("H", [1000, 5120])
+def test_one_element_apart_from_a_constant_row(moe, H):
+    """One element a step off the others: its own deviation is what is left."""
+    c = 1000.1
+    x = torch.full((1, H), c, device="cuda")
+    x[0, 17] += 0.25
+    y, mean, rstd = moe.moe_fp4_norm(x, eps=EPS, save_stats=True)
+    x64 = x.double()
+    d = x64 - x64.mean(1, keepdim=True)
+    r = 1 / torch.sqrt(d.square().mean(1, keepdim=True) + EPS)
+    # deviations off by (48 U)^2 of the mean and a step of themselves, the variance by 52 U
+    # of it and by 50 U of the first deviations' square, (48 U c)^2
+    ed = (48 * U32) ** 2 * c + 2 * U32 * d.abs()
+    ev = 52 * U32 * d.square().mean() + 50 * U32 * (48 * U32 * c) ** 2 + 2 * (d.abs() * ed).mean()
+    rel = 0.51 * ev * r * r + 8 * U32
+    assert bool(((y.double() - d * r).abs() <= 1.02 * (ed * r + (d * r).abs() * (rel + 4 * U32))).all())
