@@ -341,24 +341,24 @@ def moe_fp4_linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], w: Opti
     """(dx [M, K], dw [N, K], db [N] fp32) of moe_fp4_linear, None where not
     needed; the residual's gradient is dy.  z as moe_fp4_linear kept it (act not
     NONE); x is needed for dw, w for dx.  accumulate adds to the given dw and db."""
-    some = x if x is not None else w
-    if some is None:
-        if z is None or need_dx or need_dw:
-            raise ValueError("x is needed for dw and w for dx")
-        some = z
-    dt = some.dtype
-    if dt not in _HALF:
-        raise TypeError(f"x and w have dtype {dt}, expected one of {_HALF}")
-    if act != ACT_NONE and z is None:
-        raise ValueError("the activation's backward pass needs z")
     if (need_dx and w is None) or (need_dw and x is None):
         raise ValueError("x is needed for dw and w for dx")
+    if act != ACT_NONE and z is None:
+        raise ValueError("the activation's backward pass needs z")
     if not (need_dx or need_dw or need_db):
         raise ValueError("nothing to compute")
+    some = next((t for t in (x, w, z) if t is not None), None)
+    if some is not None:
+        dt = some.dtype
+        if dt not in _HALF:
+            raise TypeError(f"x, w and z have dtype {dt}, expected one of {_HALF}")
+    else:  # db alone: dy's type, or with an fp32 dy either of the two
+        dt = getattr(dy, "dtype", None)
+        dt = dt if dt in _HALF else torch.bfloat16
     ldy = _rows(dy, "dy", (dt, torch.float32))
     dev = dy.device
     M, N = dy.shape
-    K = some.shape[1] if some is not z else 1
+    K = x.shape[1] if x is not None else w.shape[1] if w is not None else 1
     ldx = _rows(x, "x", (dt,), dev, (M, K)) if x is not None else 0
     ldw = _rows(w, "w", (dt,), dev, (N, K)) if w is not None else 0
     ldz = _rows(z, "z", (dt,), dev, (M, N)) if z is not None else 0
