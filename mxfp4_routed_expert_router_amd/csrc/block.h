@@ -60,7 +60,7 @@ enum { kBig, kMid, kLow, kAny };
 void launch_product_fwd(const ProductArgs& a, int shape, hipStream_t stream);
 void launch_product_dgrad(const ProductArgs& a, int shape, hipStream_t stream);
 void launch_product_wgrad(const ProductArgs& a, int shape, hipStream_t stream);
-// Forward for up to m = 1, 2 or 4 rows a tile, and for 16.
+// Forward for up to m = 1, 2 or 4 rows a tile, and dense for up to 16.
 void launch_product_row(const ProductArgs& a, int m, hipStream_t stream);
 void launch_product_few(const ProductArgs& a, hipStream_t stream);
 // The most row tiles of BM rows that the experts can have.

@@ -1,7 +1,7 @@
-// The forward product of a few rows an expert (one token's experts, a decode
-// batch through a dense layer): bound by the weights' bytes.
+// The dense forward product of 5 to 16 rows (a decode batch): bound by the weights'
+// bytes.
 //
-// A workgroup takes 16 columns (16 weight rows) and 16 rows of the result; its
+// A workgroup takes 16 columns (16 weight rows) and all rows of the result; its
 // NW waves split the sum, 64 of it a unit, wave w taking the units w,
 // w + NW, ....  The weights go from memory to the registers as the matrix
 // instruction's fragments, each element once and without a stop in LDS: a wave
@@ -16,14 +16,12 @@ template <typename T, int NW, int U>
 __global__ void __launch_bounds__(NW * 64) product_few_kernel(ProductArgs g) {
   __shared__ f32x4 sums[NW][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quad = lane >> 4;
-  int e, row0, nrows;
-  if (!row_tile(g.offsets, g.E, g.P, 16, blockIdx.y, e, row0, nrows)) return;
   const int j0 = blockIdx.x * 16;
   // columns past the end read the last one's weights: their results are not stored
   const int jr = j0 + l16 < g.J ? j0 + l16 : g.J - 1;
-  const uint16_t* const w = g.b + (int64_t)e * g.w_stride + (int64_t)jr * g.ldb + quad * 8;
-  const int s = l16 < nrows ? source_row(g, row0 + l16) : -1;
-  const uint16_t* const x = g.a + (int64_t)(s < 0 ? 0 : s) * g.lda + quad * 8;
+  const uint16_t* const w = g.b + (int64_t)jr * g.ldb + quad * 8;
+  const bool live = l16 < g.P;
+  const uint16_t* const x = g.a + (int64_t)(live ? l16 : 0) * g.lda + quad * 8;
   const int units = (g.K + 63) / 64;
   f32x4 acc = {};
   for (int u0 = wave; u0 < units; u0 += NW * U) {
@@ -40,7 +38,7 @@ __global__ void __launch_bounds__(NW * 64) product_few_kernel(ProductArgs g) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int k = (u0 + u * NW) * 64 + h * 32;
-        fx[u][h] = load8(x + k, s < 0 ? 0 : g.K - k - quad * 8);
+        fx[u][h] = load8(x + k, live ? g.K - k - quad * 8 : 0);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -54,15 +52,15 @@ __global__ void __launch_bounds__(NW * 64) product_few_kernel(ProductArgs g) {
 #pragma unroll
   for (int i = 1; i < NW; ++i) v += sums[i][lane];
   const int j = j0 + quad * 4;
-  if (l16 < nrows && j < g.J) finish1(g, g.c, row0 + l16, j, 4, v);
+  if (live && j < g.J) finish1(g, g.c, l16, j, 4, v);
 }
 
 // Sixteen waves where the workgroups would leave CUs with one (N = 2304, K = 5120,
 // 16 rows: 14.2 us, 15.0 with eight).
 template <typename T>
 void launch(const ProductArgs& a, hipStream_t stream) {
-  const dim3 grid((a.J + 15) / 16, (unsigned)row_tiles_most(a, 16));
-  if ((int64_t)grid.x * grid.y <= 256)
+  const dim3 grid((a.J + 15) / 16);
+  if (grid.x <= 256)
     hipLaunchKernelGGL((product_few_kernel<T, 16, 5>), grid, dim3(1024), 0, stream, a);
   else
     hipLaunchKernelGGL((product_few_kernel<T, 8, 5>), grid, dim3(512), 0, stream, a);
