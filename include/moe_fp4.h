@@ -391,6 +391,26 @@ typedef struct {
 /* Bytes of workspace the call `op` (MOE_FP4_GROUPED_*) needs.  Errors: EINVAL, EUNSUPPORTED. */
 int moe_fp4_grouped_workspace_size(const moe_fp4_grouped_dims *dims, int op, size_t *bytes);
 
+/* Which kernels a product takes (for profiling, and for checks that depend on the
+ * order of its sums): */
+typedef struct {
+  int32_t rows;        /* 1, 2, 4: a pass over the weights, so many rows at once; */
+                       /* 16: 5 to 16 dense rows; 0: tiles (below) or nothing    */
+  int32_t tiles;       /* MOE_FP4_TILES_*, 0: none                               */
+  int32_t splits;      /* parts of the sum, joined in order                      */
+  int32_t columns;     /* columns of the result in the first launch              */
+  int32_t rest_tiles;  /* the others' launch, 0: none                            */
+  int32_t rest_splits;
+} moe_fp4_product_plan;
+#define MOE_FP4_TILES_256X256 1
+#define MOE_FP4_TILES_128X128 2
+#define MOE_FP4_TILES_64X128  3
+#define MOE_FP4_TILES_ANY     4  /* 64 x 128, rows of any length and alignment   */
+
+/* The plan of the call `op` where its pointers are on 16-byte boundaries.  Host
+ * only, enqueues nothing.  Errors: EINVAL, EUNSUPPORTED. */
+int moe_fp4_grouped_plan(const moe_fp4_grouped_dims *dims, int op, moe_fp4_product_plan *plan);
+
 /* flags: MOE_FP4_ACCUMULATE adds to the result (in fp32, rounded once).
  * Errors: EINVAL, EUNSUPPORTED (sizes, types, flags), EALIGN, EWORKSPACE, EHIP. */
 int moe_fp4_grouped_forward(const moe_fp4_grouped_dims *dims, const void *x, const void *w,
@@ -430,6 +450,10 @@ typedef struct {
 /* Bytes of workspace of moe_fp4_linear (backward = 0) or moe_fp4_linear_backward
  * (backward = 1).  Errors: EINVAL, EUNSUPPORTED. */
 int moe_fp4_linear_workspace_size(const moe_fp4_linear_dims *dims, int backward, size_t *bytes);
+
+/* The plan (above) of a product of moe_fp4_linear (op = MOE_FP4_GROUPED_FORWARD) or
+ * of moe_fp4_linear_backward: dx (MOE_FP4_GROUPED_DGRAD), dw (MOE_FP4_GROUPED_WGRAD). */
+int moe_fp4_linear_plan(const moe_fp4_linear_dims *dims, int op, moe_fp4_product_plan *plan);
 
 /* flags: MOE_FP4_ACCUMULATE adds to y.
  * Errors: EINVAL, EUNSUPPORTED (sizes, types, act, flags), EALIGN, EWORKSPACE, EHIP. */

@@ -17,6 +17,7 @@ from ._lib import (ACCUMULATE, MODE_AUTO, MODE_DECODE, MODE_PREFILL,  # noqa: F4
 from ._block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # noqa: F401
                      GROUPED_DGRAD, GROUPED_FORWARD, GROUPED_WGRAD, NORM_LAYER, NORM_RMS,
                      moe_fp4_grouped_dgrad, moe_fp4_grouped_forward, moe_fp4_grouped_wgrad,
-                     moe_fp4_grouped_workspace_size, moe_fp4_linear, moe_fp4_linear_backward,
-                     moe_fp4_linear_workspace_size, moe_fp4_norm, moe_fp4_norm_backward,
+                     moe_fp4_grouped_plan, moe_fp4_grouped_workspace_size, moe_fp4_linear, moe_fp4_linear_backward,
+                     moe_fp4_linear_plan, moe_fp4_linear_workspace_size, ProductPlan,
+                     TILES_128X128, TILES_256X256, TILES_64X128, TILES_ANY, moe_fp4_norm, moe_fp4_norm_backward,
                      moe_fp4_norm_backward_workspace_size)

@@ -19,6 +19,7 @@ F32, BF16, F16 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 NORM_LAYER, NORM_RMS = 0, 1
 GROUPED_FORWARD, GROUPED_DGRAD, GROUPED_WGRAD = range(3)
+TILES_256X256, TILES_128X128, TILES_64X128, TILES_ANY = range(1, 5)
 
 _TYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _HALF = (torch.bfloat16, torch.float16)
@@ -43,14 +44,24 @@ class NormDims(ctypes.Structure):
                 [("eps", ctypes.c_float)] + [(n, _I64) for n in ("ldx", "ldy", "lddx")])
 
 
+class ProductPlan(ctypes.Structure):
+    """Which kernels a product takes (moe_fp4_product_plan)."""
+    _fields_ = [(n, _I32) for n in ("rows", "tiles", "splits", "columns", "rest_tiles", "rest_splits")]
+
+    def __repr__(self):
+        return "ProductPlan(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
 _G, _L, _N = ctypes.POINTER(GroupedDims), ctypes.POINTER(LinearDims), ctypes.POINTER(NormDims)
 _INT = ctypes.c_int
 for _name, _args in (
         ("grouped_workspace_size", [_G, _INT, ctypes.POINTER(_SZ)]),
+        ("grouped_plan", [_G, _INT, ctypes.POINTER(ProductPlan)]),
         ("grouped_forward", [_G, _P, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
         ("grouped_dgrad", [_G, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
         ("grouped_wgrad", [_G, _P, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
         ("linear_workspace_size", [_L, _INT, ctypes.POINTER(_SZ)]),
+        ("linear_plan", [_L, _INT, ctypes.POINTER(ProductPlan)]),
         ("linear", [_L, _P, _P, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
         ("linear_backward", [_L, _P, _P, _P, _P, _P, _P, _P, _INT, _P, _SZ, _P]),
         ("norm", [_N, _P, _P, _P, _P, _P, _P, _P]),
@@ -198,6 +209,14 @@ def moe_fp4_grouped_workspace_size(E: int, P: int, N: int, K: int, op: int, dtyp
     return n.value
 
 
+def moe_fp4_grouped_plan(E: int, P: int, N: int, K: int, op: int, dtype=torch.bfloat16, out_dtype=None) -> ProductPlan:
+    """The kernels of a grouped product of dense, aligned tensors; `op` is one of GROUPED_*."""
+    d = GroupedDims(E, P, N, K, P, 1, _TYPES[dtype], _TYPES[_out_type(out_dtype, dtype)])
+    p = ProductPlan()
+    _check(_lib.moe_fp4_grouped_plan(d, op, p), "moe_fp4_grouped_plan")
+    return p
+
+
 def moe_fp4_grouped_forward(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
                             rows: Optional[torch.Tensor] = None, row_div: int = 1,
                             y: Optional[torch.Tensor] = None, out_dtype=None,
@@ -299,6 +318,18 @@ def moe_fp4_linear_workspace_size(M: int, N: int, K: int, backward: bool = False
     _check(_lib.moe_fp4_linear_workspace_size(d, int(backward), n),
            "moe_fp4_linear_workspace_size")
     return n.value
+
+
+def moe_fp4_linear_plan(M: int, N: int, K: int, op: int, dtype=torch.bfloat16, out_dtype=None, dw_dtype=None,
+                        act: int = ACT_NONE) -> ProductPlan:
+    """The kernels of a product of moe_fp4_linear (GROUPED_FORWARD) or of its backward
+    pass (GROUPED_DGRAD: dx, GROUPED_WGRAD: dw), dense, aligned tensors."""
+    t = _TYPES[dtype]
+    d = LinearDims(M, N, K, t, _TYPES[_out_type(out_dtype, dtype)], t,
+                   _TYPES[_out_type(dw_dtype, dtype, "dw_dtype")], act)
+    p = ProductPlan()
+    _check(_lib.moe_fp4_linear_plan(d, op, p), "moe_fp4_linear_plan")
+    return p
 
 
 def moe_fp4_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,

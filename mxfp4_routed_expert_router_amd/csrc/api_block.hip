@@ -19,6 +19,8 @@ static_assert(MOE_FP4_F32 == kF32 && MOE_FP4_BF16 == kBf16 && MOE_FP4_F16 == kF1
 static_assert(MOE_FP4_ACT_SILU == kActSilu && MOE_FP4_ACT_RELU == kActRelu &&
                   MOE_FP4_ACT_GELU == kActGelu && MOE_FP4_ACT_GELU_TANH == kActGeluTanh,
               "activations");
+static_assert(MOE_FP4_TILES_128X128 - MOE_FP4_TILES_256X256 == kMid && MOE_FP4_TILES_64X128 - MOE_FP4_TILES_256X256 == kLow &&
+                  MOE_FP4_TILES_ANY - MOE_FP4_TILES_256X256 == kAny && kBig == 0, "tiles");
 static_assert(MOE_FP4_GROUPED_FORWARD == kFwd && MOE_FP4_GROUPED_DGRAD == kDgrad &&
                   MOE_FP4_GROUPED_WGRAD == kWgrad, "forms");
 
@@ -81,6 +83,8 @@ int grouped_args(const moe_fp4_grouped_dims* dims, int op, bool gathered, Produc
   }
   return MOE_FP4_OK;
 }
+
+const int32_t some_offsets[1] = {0};  // for sizes and plans: their presence only, a grouped product
 
 int grouped(const moe_fp4_grouped_dims* dims, int op, const void* a, const void* b,
             const int32_t* offsets, const int32_t* rows, void* c, int flags, void* ws,
@@ -210,6 +214,23 @@ int norm_args(const moe_fp4_norm_dims* dims, NormArgs& a) {
   a.eps = d.eps;
   return MOE_FP4_OK;
 }
+// The choice for pointers on 16-byte boundaries (the strides count).
+int product_plan(const ProductArgs& a, int op, moe_fp4_product_plan* plan) {
+  *plan = moe_fp4_product_plan{};
+  if (op != kWgrad && a.P == 0) return MOE_FP4_OK;  // nothing runs
+  const ProductChoice c = product_choice(a, op);
+  plan->rows = c.rows;
+  if (c.rows) return MOE_FP4_OK;
+  plan->tiles = MOE_FP4_TILES_256X256 + c.shape;
+  plan->splits = c.splits;
+  plan->columns = c.cut;
+  if (c.cut < a.J) {
+    plan->rest_tiles = MOE_FP4_TILES_256X256 + c.rest_shape;
+    plan->rest_splits = c.rest_splits;
+  }
+  return MOE_FP4_OK;
+}
+
 size_t norm_part_bytes(const NormArgs& a) { return (size_t)norm_blocks(a) * 2 * a.H * 4; }
 
 }  // namespace
@@ -221,10 +242,18 @@ int moe_fp4_grouped_workspace_size(const moe_fp4_grouped_dims* dims, int op, siz
   ProductArgs a;
   const int rc = grouped_args(dims, op, false, a);
   if (rc != MOE_FP4_OK) return rc;
-  static const int32_t some_offsets[1] = {0};
-  a.offsets = some_offsets;  // its presence only: a grouped product
+  a.offsets = some_offsets;
   *bytes = product_workspace(a, op);
   return MOE_FP4_OK;
+}
+
+int moe_fp4_grouped_plan(const moe_fp4_grouped_dims* dims, int op, moe_fp4_product_plan* plan) {
+  if (!plan) return MOE_FP4_EINVAL;
+  ProductArgs a;
+  const int rc = grouped_args(dims, op, false, a);
+  if (rc != MOE_FP4_OK) return rc;
+  a.offsets = some_offsets;
+  return product_plan(a, op, plan);
 }
 
 int moe_fp4_grouped_forward(const moe_fp4_grouped_dims* dims, const void* x, const void* w,
@@ -253,6 +282,16 @@ int moe_fp4_linear_workspace_size(const moe_fp4_linear_dims* dims, int backward,
   *bytes = backward ? backward_layout(*dims, s).total
                     : product_workspace(linear_forward_args(*dims, s), kFwd);
   return MOE_FP4_OK;
+}
+
+int moe_fp4_linear_plan(const moe_fp4_linear_dims* dims, int op, moe_fp4_product_plan* plan) {
+  if (!plan) return MOE_FP4_EINVAL;
+  if (op < kFwd || op > kWgrad) return MOE_FP4_EUNSUPPORTED;
+  LinearStrides s;
+  const int rc = linear_check(dims, op != kFwd, s);
+  if (rc != MOE_FP4_OK) return rc;
+  return product_plan(op == kFwd ? linear_forward_args(*dims, s) : op == kDgrad ? linear_dgrad_args(*dims, s)
+                                                                                 : linear_wgrad_args(*dims, s), op, plan);
 }
 
 int moe_fp4_linear(const moe_fp4_linear_dims* dims, const void* x, const void* w, const void* bias,

@@ -57,6 +57,14 @@ hipError_t launch_product(ProductArgs a, int op, void* ws, hipStream_t stream);
 // The tile shapes of the products through LDS.  kAny takes rows of any length and
 // alignment, the others 16-byte aligned rows whose length is a multiple of 8.
 enum { kBig, kMid, kLow, kAny };
+// The kernels that launch_product takes.
+struct ProductChoice {
+  int rows;    // a tile of the streaming kernel (1, 2, 4) or the few-row kernel (16); 0: tiles through LDS
+  int shape, splits;            // of the columns up to `cut`
+  int cut;
+  int rest_shape, rest_splits;  // of the others
+};
+ProductChoice product_choice(const ProductArgs& a, int op);
 void launch_product_fwd(const ProductArgs& a, int shape, hipStream_t stream);
 void launch_product_dgrad(const ProductArgs& a, int shape, hipStream_t stream);
 void launch_product_wgrad(const ProductArgs& a, int shape, hipStream_t stream);

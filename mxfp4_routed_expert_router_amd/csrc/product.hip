@@ -187,6 +187,12 @@ void launch_tiles(ProductArgs a, int op, const Tiles& t, hipStream_t stream) {
 
 }  // namespace
 
+ProductChoice product_choice(const ProductArgs& a, int op) {
+  const Plan p = plan(a, op);
+  const bool wide = wide_rows(a, op);
+  return {p.rows, wide ? p.main.shape : kAny, p.main.splits, p.cut, wide ? p.rest.shape : kAny, p.rest.splits};
+}
+
 size_t product_workspace(const ProductArgs& a, int op) {
   if (op != kWgrad && a.P == 0) return 0;
   const Plan p = plan(a, op);
