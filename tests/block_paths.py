@@ -77,6 +77,22 @@ GROUPED = [
     ((WGRAD, 2, 2550, 927, 95), (0, ANY, 1)),
 ]
 
+# the weights' gradient with sums longer than the 1024 row indexes that it holds at a time:
+# rows of the experts, N, K, (tiles, split?)
+LONG = [1023, 0, 1024, 1025, 1, 1088, 3333, 2049]
+LONG_SUMS = [
+    ((LONG, 72, 264), (MID, 1)),
+    ((LONG, 504, 776), (MID, 0)),
+    ((LONG, 2056, 2056), (BIG, 0)),
+    ((LONG, 33, 47), (ANY, 1)),
+    ((LONG, 777, 1031), (ANY, 0)),
+    # also longer than that in each part of a split sum
+    (([9000, 1025, 0, 5000], 264, 264), (MID, 1)),
+    (([9000, 0, 7001], 265, 263), (ANY, 1)),
+    (([12000, 4668, 0], 168, 1288), (LOW, 1)),
+    (([9000], 680, 1720), (BIG, 1)),
+]
+
 
 def names(cases):
     what = ("fwd", "dgrad", "wgrad")

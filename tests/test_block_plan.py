@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from block_paths import DENSE, GROUPED, names
+from block_paths import DENSE, GROUPED, LONG_SUMS, WGRAD, names
 
 
 @pytest.fixture(scope="module")
@@ -35,6 +35,13 @@ def test_grouped(moe, case, path):
     p = moe.moe_fp4_grouped_plan(E, P, N, K, op)
     assert of(p, N if op == 0 else K) == path + (0, 0), p
     assert (moe.moe_fp4_grouped_workspace_size(E, P, N, K, op) > 0) == (p.splits > 1)
+
+
+@pytest.mark.parametrize("case,path", LONG_SUMS, ids=[f"{c[1]}x{c[2]}_{sum(c[0])}" for c, _ in LONG_SUMS])
+def test_long_sums(moe, case, path):
+    counts, N, K = case
+    p = moe.moe_fp4_grouped_plan(len(counts), sum(counts), N, K, WGRAD)
+    assert of(p, K) == (0,) + path + (0, 0), p
 
 
 def test_no_rows(moe):

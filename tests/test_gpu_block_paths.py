@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from block_common import U32, bounded, gen, offsets_of, padded, randn
-from block_paths import ANY, DENSE, DGRAD, FWD, GROUPED, WGRAD, counts_of, names
+from block_paths import ANY, DENSE, DGRAD, FWD, GROUPED, LONG_SUMS, WGRAD, counts_of, names
 from test_gpu_grouped import reference, src_rows
 from test_gpu_linear import forward64
 
@@ -155,6 +155,28 @@ def test_grouped(moe, case, path, dt, gathered, exact):
         else:
             bounded(y[lead:lead + P], want, n * U32 * mag, out, f"{out}")
         assert untouched(buf, y[lead:lead + P], 16 + lead * y.stride(0))
+
+
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("case,path", LONG_SUMS, ids=[f"{c[1]}x{c[2]}_{sum(c[0])}" for c, _ in LONG_SUMS])
+def test_long_gathered_sums(moe, case, path, dt):
+    """The weights' gradient holds 1024 row indexes at a time: sums of one less, one more and
+    several times as many, a row taken several times, some indexes outside x."""
+    counts, N, K = case
+    P, div = sum(counts), 3
+    g = gen(P + N)
+    R = P // div
+    x, dy = whole(g, R, K, dtype=dt), whole(g, P, N, dtype=dt)
+    rows = torch.randint(0, R * div, (P,), generator=g, device="cuda", dtype=torch.int32)
+    rows[11::97], rows[1023::1024], rows[1024::1024] = -5, R * div, 2 ** 31 - 1
+    off = offsets_of(counts)
+    want, _ = reference("wgrad", dy.double(), src_rows(x, rows, div, P), counts)
+    exactly(moe.moe_fp4_grouped_wgrad(dy, x, off, rows=rows, row_div=div, out_dtype=F32), want, "f32")
+    exactly(moe.moe_fp4_grouped_wgrad(dy, x, off, rows=rows, row_div=div), want, "16 bits")
+    old = whole(g, *want.shape, dtype=F32)
+    more = old.clone()
+    moe.moe_fp4_grouped_wgrad(dy, x, off, rows=rows, row_div=div, dw=more, accumulate=True)
+    exactly(more, want + old.double(), "dw +=")
 
 
 def test_unaligned_pointers_take_the_tiles_of_any_alignment(moe):
