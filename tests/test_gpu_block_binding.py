@@ -30,3 +30,20 @@ def test_bias_gradient_alone(moe, M, N, dyt):
     moe.moe_fp4_linear_backward(dy, None, None, need_dx=False, need_dw=False, db=more, accumulate=True)
     bounded(more, dy.double().sum(0) + db.double(), (M + 2) * U32 * dy.double().abs().sum(0) + U32 * db.double().abs(),
             F32, "db +=")
+
+
+def test_public_calls_for_device_and_stream(moe, monkeypatch):
+    """What a torch without the private names uses: the current stream all the same."""
+    from mxfp4_routed_expert_router_amd import _block
+    g = gen(2)
+    x, w = randn(g, 40, 256, dtype=BF), randn(g, 96, 256, dtype=BF)
+    want = moe.moe_fp4_linear(x, w)
+    s = torch.cuda.Stream()
+    monkeypatch.setattr(_block, "_device", torch.cuda.current_device)
+    seen = []
+    monkeypatch.setattr(_block, "_raw_stream", lambda i: seen.append(torch.cuda.current_stream(i).cuda_stream) or seen[-1])
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = moe.moe_fp4_linear(x, w)
+    s.synchronize()
+    assert seen == [s.cuda_stream] and torch.equal(got, want)

@@ -201,3 +201,39 @@ def test_one_element_apart_from_a_constant_row(moe, H):
     ev = 52 * U32 * d.square().mean() + 50 * U32 * (48 * U32 * c) ** 2 + 2 * (d.abs() * ed).mean()
     rel = 0.51 * ev * r * r + 8 * U32
     assert bool(((y.double() - d * r).abs() <= 1.02 * (ed * r + (d * r).abs() * (rel + 4 * U32))).all())
+
+
+def test_fp16_gradients_in_a_captured_graph(moe):
+    """The power of two is found on the device: a replay goes by the gradients of that
+    replay.  Two graphs with workspaces of their own, eager calls between."""
+    g = gen(13)
+    M, N, K = 300, 520, 264
+    x, w, z = randn(g, M, K, dtype=HF), randn(g, N, K, dtype=HF, scale=2.0 ** -12), randn(g, M, N, dtype=HF)
+    dys = [torch.zeros(M, N, device="cuda") for _ in range(2)]
+    call = lambda dy: moe.moe_fp4_linear_backward(dy, x, w, z=z, act=moe.ACT_SILU, dw_dtype=F32)
+    call(dys[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for dy in dys:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(call(dy))
+        graphs.append(graph)
+    for power in (0, 17, -40, 12, -12):
+        for i, dy in enumerate(dys):
+            dy.copy_(randn(g, M, N) * 2.0 ** (power + 3 * i))
+        want = [call(dy) for dy in dys]
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for got, ref in zip(outs, want):
+            assert all(torch.equal(a, b) for a, b in zip(got, ref)), power
+            assert all(bool(torch.isfinite(a).all()) for a in got)
+
+
+@pytest.mark.parametrize("dyt", [HF, F32], ids=["f16", "f32"])
+def test_no_rows_of_fp16_gradients(moe, dyt):
+    x, w = torch.empty(0, 64, dtype=HF, device="cuda"), torch.ones(32, 64, dtype=HF, device="cuda")
+    dy, z = torch.empty(0, 32, dtype=dyt, device="cuda"), torch.empty(0, 32, dtype=HF, device="cuda")
+    dx, dw, db = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=moe.ACT_SILU)
+    assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
