@@ -237,3 +237,29 @@ def test_no_rows_of_fp16_gradients(moe, dyt):
     dy, z = torch.empty(0, 32, dtype=dyt, device="cuda"), torch.empty(0, 32, dtype=HF, device="cuda")
     dx, dw, db = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=moe.ACT_SILU)
     assert dx.shape == (0, 64) and bool((dw == 0).all()) and bool((db == 0).all())
+
+
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("dyt", ["same", "f32"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh", "relu"])
+def test_dz_is_rounded_once(moe, act, dyt, dt):
+    """What dx and dw add to the roundings of their sums and results is dz's one rounding,
+    of half a step: a product with the identity brings out the rounded dz, and dx and dw
+    are its products."""
+    g = gen(17)
+    M, N, K = 260, 136, 328
+    a = {"none": moe.ACT_NONE, "silu": moe.ACT_SILU, "gelu": moe.ACT_GELU, "gelu_tanh": moe.ACT_GELU_TANH,
+         "relu": moe.ACT_RELU}[act]
+    x, w, z = randn(g, M, K, dtype=dt), randn(g, N, K, dtype=dt), randn(g, M, N, dtype=dt)
+    dy = randn(g, M, N, dtype=dt if dyt == "same" else F32)
+    one = torch.eye(N, device="cuda").to(dt)
+    dz, _, _ = moe.moe_fp4_linear_backward(dy, None, one, z=z, act=a, need_dw=False, need_db=False)
+    s = torch.ones_like(z.double()) if act == "none" else slope64(z.double(), act)
+    e = 0 if act in ("none", "relu") else dy.double().abs() * (16 + 8 * z.double().abs()) * U32 * 1.2  # the slope's own
+    bounded(dz, dy.double() * s, torch.zeros_like(s) + e, dt, "dz")
+    dx, dw, _ = moe.moe_fp4_linear_backward(dy, x, w, z=z, act=a, dw_dtype=F32, need_db=False)
+    dz, x, w = dz.double(), x.double(), w.double()
+    # fp16 takes steps of 2^-14 of a value below it, and dz has been 2^12 and more times itself there
+    low = 2.0 ** -14 if dt == HF else 0.0
+    bounded(dx, dz @ w, N * U32 * (dz.abs().clamp(min=low) @ w.abs().clamp(min=low)), dt, "dx")
+    bounded(dw, dz.t() @ x, M * U32 * (dz.t().abs().clamp(min=low) @ x.abs().clamp(min=low)), F32, "dw")
