@@ -480,8 +480,9 @@ int moe_fp4_linear_backward(const moe_fp4_linear_dims *dims, const void *dy, con
  *   mean = sum_h x / H (RMS: 0), rstd = 1 / sqrt(sum_h (x - mean)^2 / H + eps)
  *   y = (x - mean) * rstd * gamma + beta
  * gamma and beta may be NULL (1 and 0).  mean and rstd (fp32 [T]) are written
- * where not NULL; the backward pass reads them.  y may be x where both have
- * the same type and stride. */
+ * where not NULL; the backward pass reads them.  A row whose sum or
+ * squares' sum passes fp32 (|x| from about 1.8e19 / sqrt(H) on) has no defined
+ * result.  y may be x where both have the same type and stride. */
 #define MOE_FP4_NORM_LAYER 0
 #define MOE_FP4_NORM_RMS   1
 

@@ -20,7 +20,7 @@
 // r sit at unit ^ unit_swizzle(r).
 //
 // Bound by the matrix cores and LDS together where the rows are many: 4096^3 bf16
-// 95 us forward, 97 rows' gradient, 102 weights' gradient (1.45, 1.42 and 1.35
+// 98 us forward, 97 rows' gradient, 101 weights' gradient (1.40, 1.41 and 1.36
 // PFLOP/s; a step of 256 x 256 takes 1.5 us).  By the weights' bytes where an expert
 // has few rows: 48 experts of 2304 x 5120, 32 rows each, 205 us (5.5 TB/s).
 #pragma once
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
             row[q] = di < ni ? i0 + di : -1;
           }
           if (!part) {
-            finish<Q>(g, c, row, j, 4, v);
+            finish<Q, Factor>(g, c, row, j, 4, v);
           } else {
             const bool wide = __builtin_amdgcn_ballot_w64(g.J - j < 4) == 0;
 #pragma unroll

@@ -106,14 +106,16 @@ def test_dense_exactly(moe, case, path, dt):
             exactly(dw, dy.double().t() @ x.double() + old.double())
 
 
+# with the rows in expert order, and gathered (the rows' gradient takes them in order only)
+ROWS = [(c, p, False) for c, p in GROUPED] + [(c, p, True) for c, p in GROUPED if c[0] != DGRAD]
+ROW_IDS = names(GROUPED) + [n + "_gathered" for n in names([g for g in GROUPED if g[0][0] != DGRAD])]
+
+
 @pytest.mark.parametrize("exact", [False, True], ids=["normal", "whole"])
-@pytest.mark.parametrize("gathered", [False, True], ids=["rows", "gathered"])
 @pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
-@pytest.mark.parametrize("case,path", GROUPED, ids=names(GROUPED))
+@pytest.mark.parametrize("case,path,gathered", ROWS, ids=ROW_IDS)
 def test_grouped(moe, case, path, dt, gathered, exact):
     op, E, P, N, K = case
-    if gathered and op == DGRAD:
-        pytest.skip("takes its rows in expert order")
     g = gen(E + P + N + K)
     counts = counts_of(E, P)
     assert sum(counts) == P
