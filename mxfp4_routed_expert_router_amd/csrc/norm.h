@@ -55,8 +55,8 @@ struct Chunk {
   }
 };
 // kPast: the store passes the L2 (non-temporal).  It pays where a row is read and
-// written once: 16384 x 5120 bf16 forward 70.5 -> 67.6 us, x 2304 36.6 -> 29.5.  In
-// the backward pass it does not: f32 rows of 4096 147 -> 158 us.
+// written once: 16384 x 5120 bf16 forward 65.1 us, 67.2 without (x 2304 37.4 either
+// way).  In the backward pass it does not: f32 rows of 4096 147 -> 158 us.
 template <typename T, bool kPast>
 __device__ __forceinline__ void store_chunk(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (T::kType == kF32) {

@@ -20,7 +20,7 @@
 // r sit at unit ^ unit_swizzle(r).
 //
 // Bound by the matrix cores and LDS together where the rows are many: 4096^3 bf16
-// 98 us forward, 97 rows' gradient, 101 weights' gradient (1.40, 1.41 and 1.36
+// 95 - 98 us forward, 95 - 97 rows' gradient, 98 - 101 weights' gradient (1.4
 // PFLOP/s; a step of 256 x 256 takes 1.5 us).  By the weights' bytes where an expert
 // has few rows: 48 experts of 2304 x 5120, 32 rows each, 205 us (5.5 TB/s).
 #pragma once
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
       auto at = [&](const char* p, int have) {
         return reinterpret_cast<const u32x4_any*>(have >= 8 ? p : have > 0 ? p - 2 * (8 - have) : zero);
       };
-      if (OP == kFwd && s < full) {  // 2047 x 2303 x 5119: 138 us, 143 without
+      if (OP == kFwd && s < full) {  // 2047 x 2303 x 5119, f16: 122 us, 125 without
 #pragma unroll
         for (int n = 0; n < decltype(la_)::value; ++n)
           rega[n] = *at(from_a(n), !RowsA || rowp[RowsA ? n : 0] ? 8 : 0);
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(S::Threads, S::OCC) product_lds_kernel(Product
   // offset, four or eight rows' reads from LDS ahead of their stores: a weight
   // gradient of few rows an expert is bound by this part.  They pass the L2 (non-
   // temporal): other XCDs read them after the launch, whose end writes the L2
-  // back anyway, and 2.3 GB of weight gradients take 636 us against 776.  Parts of
+  // back anyway, and 2.3 GB of weight gradients take 611 us against 695.  Parts of
   // a split sum stay in it for the kernel that joins them (512 x 512 x 16384: 27.3
   // us against 29.1).
   constexpr int JC = S::JC, IC = S::IC, CH = JC * 4, Rows = IC * 16, RowBytes = JC * 64, At = 64 / CH, Q = 16 / At;
