@@ -516,6 +516,138 @@ int moe_fp4_norm_backward(const moe_fp4_norm_dims *dims, const void *dy, const v
                           float *dgamma, float *dbeta, int flags, void *ws, size_t ws_bytes,
                           hipStream_t stream);
 
+/* ---- the router's losses
+ * Logits l [T][E], the chosen experts idx [T][k] (moe_fp4_route's topk_idx) and the
+ * batch's sequences: sequence s is the tokens seqs[s] .. seqs[s+1]-1 (int32 [S+1] on
+ * the device, ascending; NULL with S = 1: all tokens).  mask [T] (bytes, NULL: none)
+ * leaves out tokens whose byte is 0: nothing of them is read but the byte.  With n the
+ * sequence's tokens that are left and p a token's probabilities,
+ *   SOFTMAX  p = softmax(l)        SIGMOID  p_e = sigmoid(l_e) / sum_i sigmoid(l_i)
+ *   counts[s][e] = its choices of expert e          tokens[s] = n
+ *   probs[s][e]  = sum over its tokens of p_e
+ *   balance[s]   = E / (k n^2) * sum_e counts[s][e] * probs[s][e]
+ *   z[s]         = sum over its tokens of (log sum_e exp(l_e))^2 / n
+ * An idx outside [0, E) is a dropped choice and counts nowhere; one that a token has
+ * twice counts twice.  A logit of -inf is an expert without probability; a token of
+ * such alone adds nothing to probs and z and counts as a token.  A NaN, or for SOFTMAX
+ * and z +inf, makes its token's terms NaN.  A sequence without tokens gives zeros.
+ * Tokens outside [seqs[0], seqs[S]) belong to no sequence.  seqs is held to [0, T];
+ * where it is not ascending results have no defined value, and no access leaves the
+ * arrays.
+ *
+ * Several ranks that balance over all their tokens add up counts, tokens and probs of
+ * theirs and give the sums to the backward pass: each rank's gradient is then that of
+ * E / (k n^2) sum_e counts[e] probs[e] of the sums. */
+#define MOE_FP4_SCORE_SOFTMAX 0
+#define MOE_FP4_SCORE_SIGMOID 1
+
+typedef struct {
+  int32_t T;          /* tokens: 0 .. 1048576                                 */
+  int32_t E;          /* experts: 1 .. 1024                                   */
+  int32_t k;          /* choices of a token: 1 .. min(E, 16)                  */
+  int32_t S;          /* sequences: 1 .. 65536                                */
+  int32_t score;      /* MOE_FP4_SCORE_*                                      */
+  int32_t type;       /* logits: any of the three                             */
+  int32_t out_type;   /* dlogits (backward only): MOE_FP4_F32 or `type`, any   */
+                      /* where `type` is MOE_FP4_F32                          */
+  int64_t ld, ldd;    /* logits, dlogits [T][E]                               */
+} moe_fp4_router_loss_dims;
+
+int moe_fp4_router_loss_workspace_size(const moe_fp4_router_loss_dims *dims, size_t *bytes);
+
+/* counts [S][E], tokens [S] int32; probs [S][E], balance [S], z [S] fp32: all written.
+ * Errors: EINVAL, EUNSUPPORTED (sizes, types, score), EALIGN, EWORKSPACE, EHIP. */
+int moe_fp4_router_loss(const moe_fp4_router_loss_dims *dims, const void *logits, const int32_t *idx,
+                        const int32_t *seqs, const uint8_t *mask, int32_t *counts, int32_t *tokens,
+                        float *probs, float *balance, float *z, void *ws, size_t ws_bytes,
+                        hipStream_t stream);
+
+/* The gradient of the logits: of sum_s dbalance[s] balance[s] + dz[s] z[s] (fp32 [S], either
+ * may be NULL), the choices being constants, and of the gates where `gates` is given:
+ *   dl[t][idx[t][j]] += gates[t][j] * (dgates[t][j] - sum_i gates[t][i] dgates[t][i])
+ * (fp32 [T][k], both or neither; gates as moe_fp4_route makes them).  At least one of
+ * the three is given.  logits, seqs and mask as in the forward pass; counts is read for
+ * dbalance, tokens for dbalance and dz, idx for the gates; NULL otherwise.  Rows of
+ * masked tokens are zeros, rows of no sequence are left as they were.  dlogits may be
+ * the logits (same type and stride).
+ * flags: MOE_FP4_ACCUMULATE adds to dlogits (rows of masked tokens stay).
+ * Errors: as moe_fp4_router_loss, and EUNSUPPORTED (flags). */
+int moe_fp4_router_loss_backward(const moe_fp4_router_loss_dims *dims, const void *logits,
+                                 const int32_t *idx, const int32_t *seqs, const uint8_t *mask,
+                                 const int32_t *counts, const int32_t *tokens, const float *dbalance,
+                                 const float *dz, const float *gates, const float *dgates,
+                                 void *dlogits, int flags, hipStream_t stream);
+
+/* ---- the gradients' global norm, and clipping
+ *   sumsq = sum over all tensors' elements of g^2           (fp64)
+ *   norm  = sqrt(sumsq)      factor = min(1, max_norm / (norm + eps))
+ *   out   = g * factor
+ * in two calls, so that ranks that hold parts of the gradients can add up sumsq between
+ * them.  Squares are taken and summed in fp64: no gradient of the three types is lost
+ * or overflows.  The tensors' list is host data, read during the call (a captured call
+ * keeps the addresses).  A NaN in sumsq makes every output NaN; a sumsq of inf gives a
+ * factor of 0 (NaN where g is inf or NaN).  norm tells both. */
+typedef struct {
+  void *data;         /* [n], contiguous; NULL where n = 0                    */
+  void *out;          /* moe_fp4_grad_clip: the result, NULL: data itself      */
+  int64_t n;          /* elements: 0 .. 2^40                                  */
+  int32_t type;       /* data: any of the three                               */
+  int32_t out_type;   /* out: `type`, any where `type` is MOE_FP4_F32; not read without out */
+} moe_fp4_grad_tensor;
+
+/* tensors [n_tensors], 0 .. 4096 of them (may be NULL where 0).  Errors: EINVAL, EUNSUPPORTED. */
+int moe_fp4_grad_sumsq_workspace_size(const moe_fp4_grad_tensor *tensors, int n_tensors, size_t *bytes);
+
+/* sumsq: fp64 [1], 8-byte aligned.  flags: MOE_FP4_ACCUMULATE adds to it.  out is not read.
+ * Errors: EINVAL, EUNSUPPORTED (sizes, types, flags), EALIGN, EWORKSPACE, EHIP. */
+int moe_fp4_grad_sumsq(const moe_fp4_grad_tensor *tensors, int n_tensors, double *sumsq, int flags,
+                       void *ws, size_t ws_bytes, hipStream_t stream);
+
+/* max_norm >= 0, eps >= 0; norm: fp32 [1] or NULL.  Where factor is 1, tensors clipped in
+ * place are not touched.  No written range may overlap another tensor's (EINVAL); out may
+ * be data (same type) or overlap no input.
+ * Errors: as moe_fp4_grad_sumsq. */
+int moe_fp4_grad_clip(const moe_fp4_grad_tensor *tensors, int n_tensors, const double *sumsq,
+                      float max_norm, float eps, float *norm, hipStream_t stream);
+
+/* ---- dense product with 4-bit weights and group scales, for few rows
+ *   y[m][n] = act(sum_c x[m][c] * W[n][c] + bias[n]) + residual[m][n]
+ *   MX    W[n][c] = E2M1(code) * 2^(scale - 127), a UE8M0 scale byte (2 .. 252) per 32
+ *         inputs: the experts' format (moe_fp4_weights)
+ *   INT4  W[n][c] = (code - zero) * scale, code 0 .. 15, a scale of 16 or 32 bits and a
+ *         zero (one byte, any value; 8 without zeros) per `group` inputs
+ * The low nibble of a byte holds the even input.  Products of x and the codes are exact
+ * in fp32 and summed in fp32 over a group, then times its scale; for INT4
+ * the sum of code * x less zero * the sum of x.  Made for up to 64 rows, whose
+ * time is that of the weights; more are taken 64 at a time. */
+#define MOE_FP4_W4_MX   0
+#define MOE_FP4_W4_INT4 1
+
+typedef struct {
+  int32_t M;          /* rows: 0 .. 1048576                                   */
+  int32_t N;          /* outputs: 1 .. 65536                                  */
+  int32_t K;          /* inputs: a multiple of 32 in [32, 65536]              */
+  int32_t code;       /* MOE_FP4_W4_*                                         */
+  int32_t group;      /* inputs of a scale: MX 32; INT4 32, 64, 128 or 256     */
+                      /* (the last one of a row may hold fewer)               */
+  int32_t type;       /* x: MOE_FP4_BF16 or MOE_FP4_F16                       */
+  int32_t out_type;   /* y, residual: `type` or MOE_FP4_F32                   */
+  int32_t bias_type;  /* bias: any of the three                               */
+  int32_t scale_type; /* INT4: any of the three (MX: not read)                 */
+  int32_t act;        /* MOE_FP4_ACT_*                                        */
+  int64_t ldx, ldy, ldr; /* x [M][K], y [M][N], residual                       */
+  int64_t ldw;        /* bytes between rows of codes, 0: K / 2; a multiple of 16 */
+                      /* otherwise, at least K / 2, at most 4194304           */
+} moe_fp4_w4_dims;
+
+/* codes [N][K/2] bytes, 16-byte aligned; scales [N][G] and zeros [N][G] (NULL: 8, and for
+ * MX) dense, G = ceil(K / group).  bias and residual may be NULL; y may be the residual
+ * (same stride).  flags: MOE_FP4_ACCUMULATE adds to y.
+ * Errors: EINVAL, EUNSUPPORTED (sizes, types, act, flags), EALIGN, EHIP. */
+int moe_fp4_linear_w4(const moe_fp4_w4_dims *dims, const void *x, const uint8_t *codes,
+                      const void *scales, const uint8_t *zeros, const void *bias,
+                      const void *residual, void *y, int flags, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char *moe_fp4_status_string(int status);
 

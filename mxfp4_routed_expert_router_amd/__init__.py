@@ -21,3 +21,7 @@ from ._block import (ACT_GELU, ACT_GELU_TANH, ACT_NONE, ACT_RELU, ACT_SILU,  # n
                      moe_fp4_linear_plan, moe_fp4_linear_workspace_size, ProductPlan,
                      TILES_128X128, TILES_256X256, TILES_64X128, TILES_ANY, moe_fp4_norm, moe_fp4_norm_backward,
                      moe_fp4_norm_backward_workspace_size)
+from ._train import (RouterLoss, SCORE_SIGMOID, SCORE_SOFTMAX, moe_fp4_grad_clip, moe_fp4_grad_sumsq,  # noqa: F401
+                     moe_fp4_grad_sumsq_workspace_size, moe_fp4_router_loss, moe_fp4_router_loss_backward,
+                     moe_fp4_router_loss_workspace_size)
+from ._w4 import W4Weights, moe_fp4_linear_w4  # noqa: F401

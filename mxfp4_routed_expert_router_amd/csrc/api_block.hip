@@ -5,13 +5,12 @@
 
 #include <math.h>
 
-#include "block.h"
+#include "api_common.h"
 
 using namespace moe_fp4;
 
 namespace {
 
-constexpr size_t kAlign = 256;
 constexpr int kMaxGroupedExperts = 1024;
 constexpr int kMaxNormWidth = 16384;
 
@@ -23,26 +22,6 @@ static_assert(MOE_FP4_TILES_128X128 - MOE_FP4_TILES_256X256 == kMid && MOE_FP4_T
                   MOE_FP4_TILES_ANY - MOE_FP4_TILES_256X256 == kAny && kBig == 0, "tiles");
 static_assert(MOE_FP4_GROUPED_FORWARD == kFwd && MOE_FP4_GROUPED_DGRAD == kDgrad &&
                   MOE_FP4_GROUPED_WGRAD == kWgrad, "forms");
-
-size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-size_t size_of(int type) { return type == kF32 ? 4 : 2; }
-bool type_ok(int t) { return t == kF32 || t == kBf16 || t == kF16; }
-bool is16(int t) { return t == kBf16 || t == kF16; }
-// A row stride as given (0: dense); false where rows would overlap, or where a
-// tile's byte offsets would not fit the kernels' 32 bits.
-constexpr int64_t kMaxRowStride = 1 << 22;
-bool stride(int64_t given, int width, int64_t& ld) {
-  ld = given ? given : width;
-  return ld >= width && ld <= kMaxRowStride;
-}
-int workspace_check(const void* ws, size_t have, size_t need) {
-  if (need == 0) return MOE_FP4_OK;
-  if (!ws) return MOE_FP4_EINVAL;
-  if (!aligned(ws, kAlign)) return MOE_FP4_EALIGN;
-  return have < need ? MOE_FP4_EWORKSPACE : MOE_FP4_OK;
-}
-int done(hipError_t e) { return e == hipSuccess ? MOE_FP4_OK : MOE_FP4_EHIP; }
 
 // ---- grouped products
 int grouped_args(const moe_fp4_grouped_dims* dims, int op, bool gathered, ProductArgs& a) {

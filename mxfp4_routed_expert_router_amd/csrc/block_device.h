@@ -350,6 +350,12 @@ __device__ __forceinline__ float column_sum(const float* part, int64_t width, in
   for (; p < parts; p += 8) v += part[p * width];
   return v;
 }
+// Sum over the wave's lanes in a fixed order, in every lane.
+__device__ __forceinline__ double wave_sum_f64(double v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
 __device__ __forceinline__ void* result_of(const ProductArgs& g, int e) {
   return static_cast<char*>(g.c) + (int64_t)e * g.c_stride * (g.c_type == kF32 ? 4 : 2);
 }

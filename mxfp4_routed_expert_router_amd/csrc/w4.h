@@ -1,0 +1,24 @@
+// Internal launch interface of the dense product with 4-bit weights.
+#pragma once
+
+#include "block.h"
+
+namespace moe_fp4 {
+
+enum { kMx = 0, kInt4 = 1 };  // the values of the public header
+
+struct W4Args {
+  int M, N, K;
+  int code, group, type, out_type, bias_type, scale_type, act, accumulate;
+  int64_t ldx, ldy, ldr, ldw;
+  const uint16_t* x;
+  const uint8_t* codes;
+  const void* scales;     // [N][groups]
+  const uint8_t* zeros;   // [N][groups] or null
+  const void *bias, *residual;
+  void* y;
+  int groups;             // scales of a row
+};
+hipError_t launch_w4(const W4Args& a, hipStream_t stream);
+
+}  // namespace moe_fp4
