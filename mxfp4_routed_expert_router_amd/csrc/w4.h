@@ -19,6 +19,8 @@ struct W4Args {
   void* y;
   int groups;             // scales of a row
 };
+void launch_w4_row(const W4Args& a, hipStream_t stream);  // one or two rows
+void launch_w4_hold(const W4Args& a, hipStream_t stream); // up to 16 rows; MX, int4 groups of 128 and 256
 hipError_t launch_w4(const W4Args& a, hipStream_t stream);
 
 }  // namespace moe_fp4

@@ -2,235 +2,222 @@
 // weights' bytes.
 //
 // A workgroup takes 16 NT columns (weight rows) and 16 MT rows of x; its waves split
-// the sum, 128 inputs (four groups of 32) a unit, wave w taking the units w, w + NW,
-// ....  Lane l loads 16 bytes of codes of column l % 16 for group l / 16 of the unit,
-// decodes them in registers and feeds them to the matrix cores as the B operand of
-// 16x16x32 products, x being A: a lane then holds sums of one column, whose scale
-// it can apply.  The waves' sums meet in LDS and are added in wave order.
+// the sum, each taking neighbouring units of 128 inputs (four groups of 32).  Loads go
+// out as memory lies: four lanes read 64 bytes of codes of a column, sixteen 256 bytes of a
+// row of x (in the matrix instruction's own order, neighbouring lanes in different
+// rows, a load took four times as long).  They pass through the wave's own corner of
+// LDS into 16x16x32 products, x as A and the codes, decoded in registers, as B: a lane
+// then holds sums of one column, whose scale it can apply, and a product takes one group.
+// The next unit's loads are on their way while one is computed.  The waves' sums meet in
+// LDS and are added in wave order.
 //
 // MX with bf16 x: the conversion from E2M1 takes the scale and its result is exact in
 // bf16, so that the products of all groups run into one sum.  Elsewhere (fp16 does not
-// hold all scales, a scaled int4 is not exact in 16 bits) a group has a sum of its own,
-// which the fp32 scale multiplies; its 32 inputs must then lie in one product, and
-// the four lanes of a column exchange their dwords (a 4 x 4 transposition).
-// int4 codes 0 .. 15 read as E4M3 bytes are exactly code * 2^-9 (0 to 7 as subnormals,
-// 8 to 15 in the first binade): the conversion from fp8 with the factor 2^9 gives them.
-// The zero point is taken off the sum: sum (q - z) x = sum q x - z sum x, where sum x comes
-// from a product with ones.
-#include "block_device.h"
-#include "w4.h"
+// hold all scales, a scaled int4 is not exact in 16 bits) a scale's inputs have a sum of
+// their own, which the fp32 scale multiplies.  The zero point is taken off that sum:
+// sum (q - z) x = sum q x - z sum x, where sum x comes from a product with ones.
+#include "w4_device.h"
 
 namespace moe_fp4 {
 namespace {
 
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
-// The bytes of a row of x in one product: eight values from k on, zeros past the end.
-__device__ __forceinline__ u32x4 load_x(const uint16_t* x, int k, int K, bool live) {
-  return live && k < K ? *reinterpret_cast<const u32x4_any*>(x + k) : zero4();
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t fp4_pair(uint32_t v, int byte) {
-  if constexpr (T::kType == kBf16) {
-    switch (byte) {
-      case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 0));
-      case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 1));
-      case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 2));
-      default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 3));
-    }
-  } else {
-    switch (byte) {
-      case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 0));
-      case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 1));
-      case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 2));
-      default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(v, 1.0f, 3));
-    }
-  }
-}
-template <typename T>
-__device__ __forceinline__ uint32_t fp8_pair(uint32_t v, bool high) {
-  if constexpr (T::kType == kBf16)
-    return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, true))
-                : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 512.0f, false));
-  else
-    return high ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.0f, true))
-                : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 512.0f, false));
-}
-// Eight codes, low nibble first, unscaled.
-template <typename T, int Code>
-__device__ __forceinline__ u32x4 decode8(uint32_t v) {
-  if constexpr (Code == kMx) {
-    return u32x4{fp4_pair<T>(v, 0), fp4_pair<T>(v, 1), fp4_pair<T>(v, 2), fp4_pair<T>(v, 3)};
-  } else {
-    const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
-    const uint32_t a = __builtin_amdgcn_perm(odd, even, 0x05010400u);  // codes 0 1 2 3
-    const uint32_t b = __builtin_amdgcn_perm(odd, even, 0x07030602u);  // codes 4 5 6 7
-    return u32x4{fp8_pair<T>(a, false), fp8_pair<T>(a, true), fp8_pair<T>(b, false), fp8_pair<T>(b, true)};
-  }
-}
-
-// Dword d of the lane with quad q becomes dword q of the lane with quad d (quad: l / 16).
-__device__ __forceinline__ u32x4 transpose_quads(u32x4 v) {
-  auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  return u32x4{c[0], c[1], d[0], d[1]};
-}
-
-__device__ __forceinline__ float scalar_as_f32(const void* p, int64_t i, int type) {
-  if (type == kF32) return static_cast<const float*>(p)[i];
-  const uint16_t h = static_cast<const uint16_t*>(p)[i];
-  return type == kBf16 ? Bf16::to_f32(h) : F16::to_f32(h);
-}
+// A wave's corner of LDS, bytes: the codes (64 a column, the 16-byte chunk c of column r
+// at chunk c ^ (r / 4) % 4), the rows of x (256 each, chunk c of row r at c ^ r), scales
+// and zeros as fp32 (16 a column).  Neither writes nor reads meet in a bank.
+template <int NT, int MT>
+struct Corner {
+  static constexpr int kCodes = 0, kX = NT * 1024, kScale = kX + MT * 4096, kZero = kScale + NT * 256,
+                       kBytes = kZero + NT * 256;
+};
 
 // Group is the inputs of a scale within a unit (32, 64 or 128; 256 takes 128's).
-template <typename T, int Code, int Group, int NT, int MT, int NW, int U>
-__global__ void __launch_bounds__(NW * 64) w4_kernel(W4Args g) {
-  constexpr bool kScaled = Code == kMx && T::kType == kBf16;  // scales go into the conversion
-  constexpr int kSums = 128 / Group;                          // scaled sums of a unit
-  extern __shared__ f32x4 sums[];                             // [NW][NT][MT][64]
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, quad = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
-  const uint8_t* w[NT];
-  int64_t sc[NT];
+template <typename T, int Code, int Group, int NT, int MT>
+struct Unit {
+  static constexpr bool kScaled = Code == kMx && T::kType == kBf16;  // scales go into the conversion
+  using C = Corner<NT, MT>;
+  u32x4 codes[NT], x[MT][4];
+  uint32_t scale[NT], zero[NT];  // of column lane / 4, group lane % 4, as loaded: whatever waits for a load stands in add
+
+  // Unit u (held to the last one: the loads of none past it are used).
+  __device__ __forceinline__ void load(const W4Args& g, const int (&n)[NT], const int (&m)[MT][4], int u, int units, int lane,
+                                       int shift) {
+    const int k0 = (u < units ? u : units - 1) * 128;
+    // lanes past the row's end load its first bytes, which add drops
+    const int kc = k0 + (lane & 3) * 32 < g.K ? k0 + (lane & 3) * 32 : 0;
+    const int kx = k0 + (lane & 15) * 8 < g.K ? k0 + (lane & 15) * 8 : 0;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {  // columns past the end read the last one's weights: their results are not stored
-    const int n = n0 + i * 16 + l16 < g.N ? n0 + i * 16 + l16 : g.N - 1;
-    w[i] = g.codes + n * g.ldw;
-    sc[i] = (int64_t)n * g.groups;
-  }
-  const uint16_t* x[MT];
-  bool live[MT];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    live[j] = m0 + j * 16 + l16 < g.M;
-    x[j] = g.x + (int64_t)(live[j] ? m0 + j * 16 + l16 : 0) * g.ldx;
-  }
-  f32x4 acc[NT][MT] = {};
-  const int units = (g.K + 127) / 128;
-  for (int u0 = wave; u0 < units; u0 += NW * U) {
-    u32x4 codes[U][NT];
-    float scale[U][NT][kScaled ? 1 : kSums], zero[U][NT][kSums];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = (u0 + u * NW) * 128 + quad * 32;
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-        codes[u][i] = k < g.K ? __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(w[i] + k / 2)) : zero4();
+    for (int i = 0; i < NT; ++i) {
+      codes[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(g.codes + n[i] * g.ldw + kc / 2));
+      const int64_t at = (int64_t)n[i] * g.groups + (kc >> shift);
+      if constexpr (Code == kMx) {
+        scale[i] = static_cast<const uint8_t*>(g.scales)[at];
+      } else {
+        if (g.scale_type == kF32) scale[i] = static_cast<const uint32_t*>(g.scales)[at];
+        else scale[i] = static_cast<const uint16_t*>(g.scales)[at];
+        if (g.zeros) zero[i] = g.zeros[at];
+      }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = (u0 + u * NW) * 128;
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) x[j][d] = *reinterpret_cast<const u32x4_any*>(g.x + m[j][d] * g.ldx + kx);
+  }
+
+  __device__ __forceinline__ void add(const W4Args& g, char* lds, f32x4 (&acc)[NT][MT], int u, int lane) {
+    const int k0 = u * 128, l16 = lane & 15, quad = lane >> 4;
+    if (k0 + 128 > g.K) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) codes[i] = sel4(k0 + (lane & 3) * 32 < g.K, codes[i]);
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) x[j][d] = sel4(k0 + l16 * 8 < g.K, x[j][d]);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      st16(lds + C::kCodes + i * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ quad) << 4), codes[i]);
+      float f;
+      if constexpr (Code == kMx) f = ue8m0_to_f32(scale[i]);
+      else f = g.scale_type == kF32 ? __uint_as_float(scale[i])
+                                    : g.scale_type == kBf16 ? Bf16::to_f32((uint16_t)scale[i]) : F16::to_f32((uint16_t)scale[i]);
+      *reinterpret_cast<float*>(lds + C::kScale + i * 256 + lane * 4) = f;
+      if constexpr (Code == kInt4)
+        *reinterpret_cast<float*>(lds + C::kZero + i * 256 + lane * 4) = g.zeros ? (float)zero[i] : 8.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const int r = 4 * d + quad;
+        st16(lds + C::kX + j * 4096 + r * 256 + ((l16 ^ r) << 4), x[j][d]);
+      }
+    f32x4 s[NT], z[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      s[i] = *reinterpret_cast<const f32x4*>(lds + C::kScale + i * 256 + l16 * 16);
+      if constexpr (Code == kInt4) z[i] = *reinterpret_cast<const f32x4*>(lds + C::kZero + i * 256 + l16 * 16);
+    }
+    f32x4 part[NT][MT], sx[MT];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {  // a product: group d of the unit, lane: eight inputs from 8 quad on
+      u32x4 fx[MT];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) fx[j] = ld16(lds + C::kX + j * 4096 + l16 * 256 + (((d * 4 + quad) ^ l16) << 4));
+      if (!kScaled && d % (Group / 32) == 0) {
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          sx[j] = f32x4{};
+#pragma unroll
+          for (int i = 0; i < NT; ++i) part[i][j] = f32x4{};
+        }
+      }
+      if constexpr (Code == kInt4) {
+        const uint32_t one = T::kType == kBf16 ? 0x3F803F80u : 0x3C003C00u;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) sx[j] = T::mfma(fx[j], u32x4{one, one, one, one}, sx[j]);
+      }
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(lds + C::kCodes + i * 1024 + l16 * 64 + ((d ^ (l16 >> 2)) << 4) +
+                                                              quad * 4);
         if constexpr (kScaled) {
-          const int at = k / 32 + quad < g.groups ? k / 32 + quad : 0;
-          scale[u][i][0] = ue8m0_to_f32(static_cast<const uint8_t*>(g.scales)[sc[i] + at]);
-        } else {
+          const u32x4 b = __builtin_bit_cast(u32x4, fp4x8_to_bf16x8(c, s[i][d]));
 #pragma unroll
-          for (int s = 0; s < kSums; ++s) {
-            const int of = (k + s * Group) / g.group, at = of < g.groups ? of : 0;
-            if constexpr (Code == kMx) {
-              scale[u][i][s] = ue8m0_to_f32(static_cast<const uint8_t*>(g.scales)[sc[i] + at]);
-            } else {
-              scale[u][i][s] = scalar_as_f32(g.scales, sc[i] + at, g.scale_type);
-              zero[u][i][s] = g.zeros ? (float)g.zeros[sc[i] + at] : 8.0f;
-            }
-          }
+          for (int j = 0; j < MT; ++j) acc[i][j] = T::mfma(fx[j], b, acc[i][j]);
+        } else {
+          const u32x4 b = decode8<T, Code>(c);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) part[i][j] = T::mfma(fx[j], b, part[i][j]);
         }
       }
-    }
+      if (!kScaled && (d + 1) % (Group / 32) == 0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k0 = (u0 + u * NW) * 128;
-      if (k0 >= g.K) break;
-      if constexpr (kScaled) {
-        // product d takes dword d of every lane: inputs k0 + 32 quad + 8 d ..
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          u32x4 fx[MT];
-#pragma unroll
-          for (int j = 0; j < MT; ++j) fx[j] = load_x(x[j], k0 + quad * 32 + d * 8, g.K, live[j]);
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            const u32x4 b = __builtin_bit_cast(u32x4, fp4x8_to_bf16x8(codes[u][i][d], scale[u][i][0]));
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = T::mfma(fx[j], b, acc[i][j]);
+          for (int j = 0; j < MT; ++j) {
+            const int first = d + 1 - Group / 32;  // past the row's end only the scale's first group is sure
+            f32x4 v = part[i][j];
+            if constexpr (Code == kInt4) v -= z[i][first] * sx[j];
+            acc[i][j] += s[i][first] * v;
           }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) codes[u][i] = transpose_quads(codes[u][i]);
-#pragma unroll
-        for (int s = 0; s < kSums; ++s) {
-          f32x4 part[NT][MT] = {}, sx[MT] = {};
-#pragma unroll
-          for (int d = s * Group / 32; d < (s + 1) * Group / 32; ++d) {  // product d: inputs k0 + 32 d + 8 quad ..
-            u32x4 fx[MT];
-#pragma unroll
-            for (int j = 0; j < MT; ++j) fx[j] = load_x(x[j], k0 + d * 32 + quad * 8, g.K, live[j]);
-            if constexpr (Code == kInt4) {
-              const uint32_t one = T::kType == kBf16 ? 0x3F803F80u : 0x3C003C00u;
-#pragma unroll
-              for (int j = 0; j < MT; ++j) sx[j] = T::mfma(fx[j], u32x4{one, one, one, one}, sx[j]);
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              const u32x4 b = decode8<T, Code>(codes[u][i][d]);
-#pragma unroll
-              for (int j = 0; j < MT; ++j) part[i][j] = T::mfma(fx[j], b, part[i][j]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              f32x4 v = part[i][j];
-              if constexpr (Code == kInt4) v -= zero[u][i][s] * sx[j];
-              acc[i][j] += scale[u][i][s] * v;
-            }
-        }
       }
     }
   }
+};
+
+template <typename T, int Code, int Group, int NT, int MT, int NW>
+__global__ void __launch_bounds__(NW * 64) w4_kernel(W4Args g, int shift) {
+  using C = Corner<NT, MT>;
+  constexpr int kSums = NW * NT * MT * 1024, kCorners = NW * C::kBytes;
+  __shared__ char lds[kSums > kCorners ? kSums : kCorners];  // the corners, then the waves' sums [NW][NT][MT][64]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16 * NT, m0 = blockIdx.y * 16 * MT;
+  // columns and rows past the end read the last one's: their results are not stored
+  int n[NT], m[MT][4];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) n[i] = n0 + i * 16 + (lane >> 2) < g.N ? n0 + i * 16 + (lane >> 2) : g.N - 1;
+#pragma unroll
+  for (int j = 0; j < MT; ++j)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const int r = m0 + j * 16 + d * 4 + (lane >> 4);
+      m[j][d] = r < g.M ? r : g.M - 1;
+    }
+  f32x4 acc[NT][MT] = {};
+  const int units = (g.K + 127) / 128, per = (units + NW - 1) / NW;
+  const int u0 = wave * per, u1 = u0 + per < units ? u0 + per : units;
+  char* const corner = lds + wave * C::kBytes;
+  Unit<T, Code, Group, NT, MT> a, b;
+  if (u0 < u1) a.load(g, n, m, u0, units, lane, shift);
+  for (int u = u0; u < u1; u += 2) {
+    b.load(g, n, m, u + 1, units, lane, shift);
+    a.add(g, corner, acc, u, lane);
+    if (u + 1 >= u1) break;
+    a.load(g, n, m, u + 2, units, lane, shift);
+    b.add(g, corner, acc, u + 1, lane);
+  }
+  __syncthreads();
+  f32x4* const sums = reinterpret_cast<f32x4*>(lds);
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) sums[((wave * NT + i) * MT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
   // thread -> column n0 + 16 i + c, row m0 + 16 j + r; lane 16 (r / 4) + c held it in component r % 4
-  const float* const f = reinterpret_cast<const float*>(sums);
+  const float* const f = reinterpret_cast<const float*>(lds);
   for (int o = threadIdx.x; o < NT * MT * 256; o += NW * 64) {
     const int c = o & 15, i = (o >> 4) % NT, r16 = (o >> 4) / NT, r = r16 & 15, j = r16 >> 4;
-    const int m = m0 + j * 16 + r, n = n0 + i * 16 + c;
-    if (m >= g.M || n >= g.N) continue;
+    const int row = m0 + j * 16 + r, col = n0 + i * 16 + c;
+    if (row >= g.M || col >= g.N) continue;
     const int at = ((i * MT + j) * 64 + 16 * (r >> 2) + c) * 4 + (r & 3);
     float v = f[at];
 #pragma unroll
     for (int q = 1; q < NW; ++q) v += f[at + q * NT * MT * 256];
-    if (g.bias) v += scalar_as_f32(g.bias, n, g.bias_type);
-    v = activate(v, g.act);
-    if (g.residual) v += scalar_as_f32(g.residual, m * g.ldr + n, g.out_type);
-    const int64_t y = m * g.ldy + n;
-    if (g.accumulate) v += scalar_as_f32(g.y, y, g.out_type);
-    if (g.out_type == kF32) static_cast<float*>(g.y)[y] = v;
-    else static_cast<uint16_t*>(g.y)[y] = T::from_f32(v);
+    finish_w4<T>(g, row, col, v);
   }
 }
 
-template <typename T, int Code, int Group, int NT, int MT, int NW, int U>
+template <typename T, int Code, int Group, int NT, int MT, int NW>
 void launch_tiles(const W4Args& a, hipStream_t stream) {
   const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (a.M + 16 * MT - 1) / (16 * MT));
-  hipLaunchKernelGGL((w4_kernel<T, Code, Group, NT, MT, NW, U>), grid, dim3(NW * 64), NW * NT * MT * 1024, stream, a);
+  int shift = 5;  // of inputs to scales
+  while (1 << shift < a.group) ++shift;
+  hipLaunchKernelGGL((w4_kernel<T, Code, Group, NT, MT, NW>), grid, dim3(NW * 64), 0, stream, a, shift);
 }
 
+// Tiles by time (one MI355X, bf16 x, MX, weights cold, us; NT MT NW):
+//   16 rows   N = 288: 1 1 8 6.8, 2 1 8 9.2; 5120 x 9216: 20.9, 17.2; 9216 x 5120: 19.5, 20.0
+//   24 rows   2304 x 5120: 1 1 8 11.2, 2 1 8 9.8, 2 2 4 12.5; 9216 x 5120: 27.6, 26.5, 23.2; 4 4 4 28.7
+//   64 rows   N = 288: 1 1 8 8.5, 2 2 4 12.8; 5120 x 5120: 30.4, 22.5, 4 4 4 30.4; 9216 x 5120: 54.0, 34.9, 31.4
 template <typename T, int Code, int Group>
 void launch_rows(const W4Args& a, hipStream_t stream) {
-  if (a.M <= 16) launch_tiles<T, Code, Group, 1, 1, 8, 2>(a, stream);
-  else launch_tiles<T, Code, Group, 2, 4, 8, 1>(a, stream);
+  if (a.N <= 512) launch_tiles<T, Code, Group, 1, 1, 8>(a, stream);
+  else if (a.M <= 16) {
+    // two columns' tiles where that fills the CUs about once, or many times
+    if ((a.N > 4096 && a.N <= 8192) || a.N >= 16384) launch_tiles<T, Code, Group, 2, 1, 8>(a, stream);
+    else launch_tiles<T, Code, Group, 1, 1, 8>(a, stream);
+  } else if (a.M <= 32 || a.N <= 8192) launch_tiles<T, Code, Group, 2, 2, 4>(a, stream);
+  else launch_tiles<T, Code, Group, 4, 4, 4>(a, stream);
 }
 
 template <typename T>
@@ -243,8 +230,15 @@ void launch_type(const W4Args& a, hipStream_t stream) {
 
 }  // namespace
 
+// One and two rows stream the weights by vector products from K = 1024 on (one row of
+// 9216 x 5120: 8.0 us, on the matrix cores 13.2; two 11.4, 13.2; four 17.0, 13.4; one of
+// 5120 x 512: 3.7, 3.1); up to 16 rows of many columns are held in registers (16 rows of
+// 65536 x 5120: 54 us, 74 through the tiles; of 9216 x 5120 with 3 rows 14.6, 13.4), where
+// a wave's scales fit beside them.
 hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
-  if (a.type == kBf16) launch_type<Bf16>(a, stream);
+  if (a.M <= 2 && a.K >= 1024) launch_w4_row(a, stream);
+  else if (a.M <= 16 && a.N >= 16384 && (a.code == kMx || a.group >= 128)) launch_w4_hold(a, stream);
+  else if (a.type == kBf16) launch_type<Bf16>(a, stream);
   else launch_type<F16>(a, stream);
   return hipGetLastError();
 }

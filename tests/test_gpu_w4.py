@@ -125,6 +125,25 @@ def test_scales_at_their_ends(moe, dt):
     check(moe, small, w, *weights64(w), F32)
 
 
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(3, 16384, 32), (16, 16385, 96), (7, 16400, 1184), (16, 20001, 2080), (5, 65536, 160),
+                                   (11, 16384, 4992), (4, 16389, 5152), (16, 16384, 10336)])
+def test_many_columns(moe, M, N, K, kind, dt):
+    """Wide weights, whose short last tile overlaps the one before; sums of one to three chunks."""
+    g = gen(M + N + K)
+    x = randn(g, M, K, dtype=dt)
+    w, w64, mag = weights(moe, g, N, K, kind, zeros=kind[0] == "int4" and M % 2 == 1)
+    check(moe, x, w, w64, mag, F32)
+    check(moe, x, w, w64, mag, dt if kind[0] == "mx" else F32, act="silu", bias=randn(g, N, dtype=BF))
+    r = randn(g, M, N)
+    y, buf = padded(r, 3, 1, fill=7.0)
+    check(moe, x, w, w64, mag, F32, residual=r, y=y)
+    left = buf.clone()
+    left.as_strided(y.shape, y.stride(), 1).fill_(7.0)
+    assert bool((left == 7.0).all())
+
+
 def test_zero_points_of_any_byte(moe):
     g = gen(5)
     for kind in KINDS[1:]:
