@@ -95,10 +95,9 @@ def moe_fp4_router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: int
     d = RouterLossDims(T, E, k, S, score, _TYPES[logits.dtype], 0, ld)
     ws, nws, keep = _workspace(_lib.moe_fp4_router_loss_workspace_size, d, workspace=workspace, device=dev)
     # one allocation for the five results
-    whole = torch.empty(S * (2 * E + 3), dtype=torch.float32, device=dev)
-    counts, tokens = whole[:S * E].view(torch.int32).view(S, E), whole[S * E:S * E + S].view(torch.int32)
-    probs = whole[S * E + S:2 * S * E + S].view(S, E)
-    balance, z = whole[2 * S * E + S:2 * S * E + 2 * S], whole[2 * S * E + 2 * S:]
+    counts, tokens, probs, balance, z = torch.empty(S * (2 * E + 3), dtype=torch.float32, device=dev).split(
+        (S * E, S, S * E, S, S)) if S > 0 else [logits.new_empty(0)] * 5
+    counts, tokens, probs = counts.view(torch.int32).view(-1, E), tokens.view(torch.int32), probs.view(-1, E)
     _call(_lib.moe_fp4_router_loss, dev, d, logits.data_ptr(), topk_idx.data_ptr(), _opt(seqs), _opt(mask),
           counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), balance.data_ptr(), z.data_ptr(), ws, nws)
     return RouterLoss(counts, tokens, probs, balance, z)

@@ -118,8 +118,7 @@ int moe_fp4_router_loss(const moe_fp4_router_loss_dims* dims, const void* logits
   a.probs = probs;
   a.balance = balance;
   a.z = z;
-  a.part = static_cast<float*>(ws);
-  return done(launch_router_loss(a, stream));
+  return done(launch_router_loss(a, ws, stream));
 }
 
 int moe_fp4_router_loss_backward(const moe_fp4_router_loss_dims* dims, const void* logits,

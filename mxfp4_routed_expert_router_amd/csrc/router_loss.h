@@ -21,8 +21,11 @@ struct RouterLossArgs {
   // forward
   int32_t *counts, *tokens;            // [S][E], [S]
   float *probs, *balance, *z;          // [S][E], [S], [S]
-  float* part;                         // [pieces_most][loss_row(E)]
-  int tokens_of_block;                 // set by launch_router_loss
+  // set by launch_router_loss
+  int tokens_of_block;
+  float* part;                         // rows of a workgroup's piece of a sequence
+  double* dots;                        // [S][E / 32, rounded up]
+  int32_t* tickets;                    // [S]
   // backward
   const int32_t *counts_in, *tokens_in;
   const float *dbalance, *dz;          // [S], or null
@@ -32,7 +35,7 @@ struct RouterLossArgs {
 };
 
 size_t router_loss_workspace(const RouterLossArgs& a);
-hipError_t launch_router_loss(RouterLossArgs a, hipStream_t stream);
+hipError_t launch_router_loss(RouterLossArgs a, void* ws, hipStream_t stream);
 hipError_t launch_router_loss_backward(RouterLossArgs a, hipStream_t stream);
 
 }  // namespace moe_fp4

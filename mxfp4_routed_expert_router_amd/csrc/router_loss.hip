@@ -9,18 +9,20 @@
 //   dl_e = p_e (c_e - sum_i p_i c_i) [softmax], times 1 - sigmoid(l_e) [sigmoid]
 //        + 2 dz lse softmax_e / n + the gates' part at the chosen experts.
 //
-// Both passes read the logits once and are bound by those bytes.  A wave takes a
-// token, lane l the columns 128 c + 2 l and + 1, so that a lane keeps the same
-// columns for every token: the sums over tokens stay in registers, and so do the
-// coefficients c of the backward pass.
+// Both passes read the logits once.  L lanes (32 from 129 to 512 experts) take a token, 64 / L
+// tokens a wave: a row's maximum and sums are then a few exchanges between neighbouring
+// lanes for several tokens at once (with a wave a token they and the exponentials took
+// more time than the bytes).  A lane keeps the same columns for every token: the sums
+// over tokens stay in registers, and so do the coefficients c of the backward pass.
 #include "block_device.h"
 #include "router_loss.h"
 
 namespace moe_fp4 {
 namespace {
 
-constexpr int kLossWaves = 8;
-constexpr int kLossBlocks = 512;  // most workgroups of the forward pass: two a CU
+constexpr int kLossWaves = 8, kLossThreads = kLossWaves * 64;
+constexpr int kLossBlocks = 256;  // most workgroups of the forward pass
+constexpr int kAloneTokens = 128, kAloneSequences = 8;  // what one workgroup finishes alone
 
 // A row of partial results: the sums of p, the counts, z's sum, the tokens.
 __host__ __device__ inline int64_t loss_row(int E) { return 2 * (int64_t)E + 2; }
@@ -32,157 +34,296 @@ __device__ __forceinline__ int seq_at(const RouterLossArgs& g, int s) {
   const int v = g.seqs[s];
   return v < 0 ? 0 : v > g.T ? g.T : v;
 }
-// The first sequence that ends past token t (S where none does).
-__device__ __forceinline__ int seq_of(const RouterLossArgs& g, int t) {
+// The first sequence that ends past token t (S where none does), found by L lanes that
+// agree on t: L places at a time.  l: the lane among them.
+template <int L>
+__device__ __forceinline__ int seq_of(const RouterLossArgs& g, int t, int l) {
+  if (!g.seqs) return t < g.T ? 0 : 1;
   int lo = 0, hi = g.S;
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seq_at(g, mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+    const int step = (hi - lo + L - 1) / L, s = lo + l * step;
+    const uint64_t before = __ballot(s < hi && seq_at(g, s + 1 <= g.S ? s + 1 : g.S) <= t) >> ((threadIdx.x & 63) - l);
+    const int c = __popcll(L == 64 ? before : before & ((1ull << (L & 63)) - 1));
+    if (c == 0) return lo;
+    const int end = lo + c * step;
+    lo += (c - 1) * step + 1;
+    hi = end < hi ? end : hi;
   }
   return lo;
 }
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef f32x2 __attribute__((aligned(4))) f32x2_word;
-typedef uint32_t __attribute__((aligned(2))) u32_half;
+// ---- a token's logits: lane `l` of its L lanes holds columns 4 (c L + l) + r, r < 4, as
+// element 4 c + r of N
+template <int L>
+__device__ __forceinline__ int column_of(int l, int i) {
+  return (i / 4 * L + l) * 4 + i % 4;
+}
 
-// Columns j and j + 1 of a row, -inf past the last.
-template <typename T>
-__device__ __forceinline__ f32x2 load_pair(const void* p, int64_t row, int j, int E) {
-  f32x2 v = {-INFINITY, -INFINITY};
-  if constexpr (T::kType == kF32) {
-    const float* const q = static_cast<const float*>(p) + row + j;
-    if (j + 1 < E) v = *reinterpret_cast<const f32x2_word*>(q);
-    else if (j < E) v[0] = *q;
-  } else {
-    const uint16_t* const q = static_cast<const uint16_t*>(p) + row + j;
-    if (j + 1 < E) {
-      const uint32_t h = *reinterpret_cast<const u32_half*>(q);
-      v = f32x2{T::to_f32((uint16_t)h), T::to_f32((uint16_t)(h >> 16))};
-    } else if (j < E) {
-      v[0] = T::to_f32(*q);
+// A row as loaded: what waits for the load is values().  -inf past the last column.
+template <typename T, int L, int N>
+struct Row {
+  static constexpr int kWords = T::kType == kF32 ? 4 : 2;
+  typedef uint32_t Words __attribute__((ext_vector_type(kWords)));
+  Words raw[N / 4];
+
+  __device__ __forceinline__ void load(const void* p, int64_t row, int l, int E) {
+#pragma unroll
+    for (int c = 0; c < N / 4; ++c) {
+      const int j = (c * L + l) * 4;
+      if constexpr (T::kType == kF32) {
+        const float* const q = static_cast<const float*>(p) + row + j;
+        if (j + 4 <= E) {
+          raw[c] = __builtin_bit_cast(Words, *reinterpret_cast<const f32x4_word*>(q));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[c][i] = __float_as_uint(j + i < E ? q[i] : -INFINITY);
+        }
+      } else {
+        constexpr uint32_t none = T::kType == kBf16 ? 0xFF80u : 0xFC00u;  // -inf
+        const uint16_t* const q = static_cast<const uint16_t*>(p) + row + j;
+        if (j + 4 <= E) {
+          raw[c] = *reinterpret_cast<const u32x2_any*>(q);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            raw[c][i] = (j + 2 * i < E ? q[2 * i] : none) | (j + 2 * i + 1 < E ? q[2 * i + 1] : none) << 16;
+        }
+      }
     }
   }
+  // What was made of the row is made anew behind this.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int c = 0; c < N / 4; ++c) asm volatile("" : "+v"(raw[c]));
+  }
+  __device__ __forceinline__ void values(float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (T::kType == kF32) v[i] = __uint_as_float(raw[i / 4][i % 4]);
+      else v[i] = T::to_f32((uint16_t)(raw[i / 4][i % 4 / 2] >> (16 * (i & 1))));
+    }
+  }
+};
+
+template <typename TO, int L, int N>
+__device__ __forceinline__ void store_row(void* p, int64_t row, int l, int E, const float (&d)[N], bool accumulate) {
+#pragma unroll
+  for (int c = 0; c < N / 4; ++c) {
+    const int j = (c * L + l) * 4, n = E - j < 4 ? E - j : 4;
+    if (n <= 0) continue;
+    f32x4 v = {d[c * 4], d[c * 4 + 1], d[c * 4 + 2], d[c * 4 + 3]};
+    if (accumulate) v += load4_as_f32(p, row + j, n, TO::kType, n == 4);
+    store4_from_f32(p, row + j, n, TO::kType, n == 4, v);
+  }
+}
+
+// ---- over the L lanes of a token, the result in each of them
+__device__ __forceinline__ float swap16(float v, bool high) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(high ? r[1] : r[0]);
+}
+__device__ __forceinline__ float swap32(float v, bool high) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(high ? r[1] : r[0]);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float(dpp_u32<CTRL>(__float_as_uint(v)));
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, dpp_f32<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = fmaxf(v, dpp_f32<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = fmaxf(v, dpp_f32<0x124>(v));  // row_ror:4
+  v = fmaxf(v, dpp_f32<0x128>(v));  // row_ror:8
+  if constexpr (L >= 32) v = fmaxf(swap16(v, false), swap16(v, true));
+  if constexpr (L >= 64) v = fmaxf(swap32(v, false), swap32(v, true));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += dpp_f32<0xB1>(v);
+  v += dpp_f32<0x4E>(v);
+  v += dpp_f32<0x124>(v);
+  v += dpp_f32<0x128>(v);
+  if constexpr (L >= 32) v = swap16(v, false) + swap16(v, true);
+  if constexpr (L >= 64) v = swap32(v, false) + swap32(v, true);
   return v;
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-  v = fmaxf(v, __uint_as_float(dpp_u32<0xB1>(__float_as_uint(v))));
-  v = fmaxf(v, __uint_as_float(dpp_u32<0x4E>(__float_as_uint(v))));
-  v = fmaxf(v, __uint_as_float(dpp_u32<0x124>(__float_as_uint(v))));
-  v = fmaxf(v, __uint_as_float(dpp_u32<0x128>(__float_as_uint(v))));
-  const float r0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 0));
-  const float r1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 16));
-  const float r2 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 32));
-  const float r3 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 48));
-  return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
-}
-
-// A token's scores: soft = exp(l - m), or, with sigmoids, `p` their values times a
-// common power; sum and soft_sum their sums.  For logits that are all negative the
-// sigmoids are taken as e^(l - m) / (1 + e^l), so that their quotients keep their
-// digits where the sigmoids themselves would be 0 in fp32.  A row of -inf alone has
-// no probabilities: its sums are 0, and so are their reciprocals and its lse.
-template <int NC>
+// A token's scores, p times a common factor: softmax e = exp(l - m), m the row's largest logit.
+//
+// Sigmoids: m = min(largest, 0), e = exp(min(l, 60) - m) and down = 1 / (1 + e e^m): p = e down is
+// sigmoid(l) e^-m, which keeps its digits where all logits are far below 0, and down is 1 - sigmoid(l),
+// from one exponential and one reciprocal.  From 60 on the sigmoid is 1 in fp32; where a row has such
+// logits (`far`) 1 - sigmoid is e^-l there, and the softmax of the z loss takes exponentials of its own.
+//
+// A row of -inf alone has no probabilities: its sums are 0, and so are their reciprocals and
+// its lse.
+constexpr float kFar = 60.f;
+template <int N, bool Sigmoid>
 struct Scores {
-  f32x2 soft[NC], p[NC], down[NC];  // down: 1 - sigmoid
-  float inv, soft_inv, lse;
-};
-template <int NC>
-__device__ __forceinline__ void scores(const f32x2 (&l)[NC], bool sigmoid, Scores<NC>& o) {
-  float m = -INFINITY;
+  float e[N], down[Sigmoid ? N : 1];
+  float inv, soft_inv, lse, top;
+  bool far;
+
+  template <int L>
+  __device__ __forceinline__ void of(const float (&l)[N]) {
+    top = l[0];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) m = fmaxf(m, fmaxf(l[c][0], l[c][1]));
-  m = wave_max_f32(m);
-  if (m == -INFINITY) m = 0.f;
-  float soft_sum = 0.f, sum = 0.f;
+    for (int i = 1; i < N; ++i) top = fmaxf(top, l[i]);
+    top = lanes_max<L>(top);
+    float m = top == -INFINITY ? 0.f : top, soft_sum = 0.f, sum = 0.f;
+    far = Sigmoid && !(top <= kFar);  // NaN too
+    if constexpr (Sigmoid) m = fminf(m, 0.f);
 #pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      o.soft[c][i] = exp_f32(l[c][i] - m);
-      soft_sum += o.soft[c][i];
+    for (int i = 0; i < N; ++i) {
+      e[i] = exp_f32((Sigmoid ? (l[i] > kFar ? kFar : l[i]) : l[i]) - m);
+      soft_sum += e[i];
     }
-  soft_sum = wave_sum_f32(soft_sum);
-  o.soft_inv = soft_sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(soft_sum);
-  o.lse = soft_sum == 0.f ? 0.f : m + __builtin_amdgcn_logf(soft_sum) * 0.6931471805599453f;
-  if (!sigmoid) {
+    if constexpr (Sigmoid) {
+      const float f = exp_f32(m);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      o.p[c] = o.soft[c];
-      o.down[c] = f32x2{1.f, 1.f};
+      for (int i = 0; i < N; ++i) {
+        down[i] = __builtin_amdgcn_rcpf(1.0f + e[i] * f);
+        sum += e[i] * down[i];
+      }
+      sum = lanes_sum<L>(sum);
+      if (far) {
+        soft_sum = 0.f;
+        m = top;
+#pragma unroll
+        for (int i = 0; i < N; ++i) soft_sum += exp_f32(l[i] - top);
+      }
     }
-    o.inv = o.soft_inv;
-    return;
+    soft_sum = lanes_sum<L>(soft_sum);
+    soft_inv = soft_sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(soft_sum);
+    lse = soft_sum == 0.f ? 0.f : m + __builtin_amdgcn_logf(soft_sum) * 0.6931471805599453f;
+    inv = !Sigmoid ? soft_inv : sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
   }
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float v = l[c][i], t = exp_f32(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + t), low = t * r;
-      o.p[c][i] = m < 0.f ? o.soft[c][i] * r : v < 0.f ? low : r;
-      o.down[c][i] = v < 0.f ? r : low;
-      sum += o.p[c][i];
-    }
-  sum = wave_sum_f32(sum);
-  o.inv = sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(sum);
+  __device__ __forceinline__ float p(int i) const {
+    if constexpr (Sigmoid) return e[i] * down[i];
+    else return e[i];
+  }
+};
+
+// What a workgroup has of a piece of a sequence goes to a row of `part`, or is finished.
+__device__ __forceinline__ void finish_loss(const RouterLossArgs& g, int s, double dot, double zz, int n) {
+  const double m = n > 0 ? n : 1;
+  g.tokens[s] = n;
+  g.balance[s] = (float)(dot * g.E / (g.k * m * m));
+  g.z[s] = (float)(zz / m);
 }
 
 // Workgroup b takes the tokens [b B, (b + 1) B), B = tokens_of_block, one piece for
 // each sequence among them.  Piece (b, s) writes row b + s of `part`: along the
-// pieces b or s grows, so that no two share a row.
-template <typename T, int NC>
-__global__ void __launch_bounds__(kLossWaves * 64) router_loss_kernel(RouterLossArgs g) {
-  __shared__ f32x2 sums[kLossWaves][NC * 64];
-  __shared__ int32_t counts[NC * 128];
+// pieces b or s grows, so that no two share a row.  One workgroup alone takes every
+// sequence, also those without tokens, and writes the results.
+template <typename T, int L, int N, bool Sigmoid>
+__global__ void __launch_bounds__(kLossThreads) router_loss_kernel(RouterLossArgs g, bool alone) {
+  constexpr int kTokens = 64 / L;  // of a wave at a time
+  __shared__ float sums[kLossWaves][L * N];  // element i of lane l at i L + l
+  __shared__ int32_t counts[L * N];
   __shared__ float zsum[kLossWaves];
   __shared__ int32_t tokens[kLossWaves];
+  __shared__ double dots[kLossWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l = lane % L, group = lane / L;
   const int t0 = blockIdx.x * g.tokens_of_block;
   const int t1 = g.T - t0 < g.tokens_of_block ? g.T : t0 + g.tokens_of_block;
-  for (int s = seq_of(g, t0); s < g.S; ++s) {
+  if (blockIdx.x == 0 && !alone)
+    for (int s = threadIdx.x; s < g.S; s += kLossThreads) g.tickets[s] = 0;
+  for (int s = alone ? 0 : seq_of<64>(g, t0, lane), next; s < g.S; s = next) {
     int lo = seq_at(g, s), hi = seq_at(g, s + 1);
-    if (lo >= t1) break;
+    if (!alone && lo >= t1) break;
     lo = lo < t0 ? t0 : lo;
     hi = hi > t1 ? t1 : hi;
-    if (lo >= hi) continue;
-    for (int e = threadIdx.x; e < NC * 128; e += kLossWaves * 64) counts[e] = 0;
-    __syncthreads();
-    for (int p = threadIdx.x; p < (hi - lo) * g.k; p += kLossWaves * 64) {
-      const int t = lo + p / g.k;
+    next = s + 1;
+    if (hi <= lo) {
+      if (!alone) {  // past the empty ones
+        const int after = seq_of<64>(g, lo, lane);
+        next = after > next ? after : next;
+        continue;
+      }
+      hi = lo;
+    }
+    // a token a turn for each group of lanes, the next one's logits on their way
+    constexpr int kTurn = kLossWaves * kTokens;
+    const auto load = [&](int t, Row<T, L, N>& r, bool& live) {
+      live = t < hi;
+      const int at = live ? t : lo;
+      if (hi > lo) r.load(g.logits, at * g.ld, l, g.E);
+      if (g.mask && live) live = g.mask[at];
+    };
+    Row<T, L, N> row[2];
+    bool live[2];
+    const int pairs = (hi - lo) * g.k;
+    const auto choice = [&](int p) {  // the expert of a choice, -1 where it does not count
+      if (p >= pairs || (g.mask && !g.mask[lo + p / g.k])) return -1;
       const int e = g.idx[(int64_t)lo * g.k + p];
-      if ((!g.mask || g.mask[t]) && e >= 0 && e < g.E) atomicAdd(&counts[e], 1);
+      return e < g.E ? e : -1;
+    };
+    load(lo + wave * kTokens + group, row[0], live[0]);
+    for (int e = threadIdx.x; e < L * N; e += kLossThreads) counts[e] = 0;
+    lds_barrier();
+    for (int p = threadIdx.x; p < pairs; p += kLossThreads) {
+      const int e = choice(p);
+      if (e >= 0) atomicAdd(&counts[e], 1);
     }
-    f32x2 acc[NC] = {};
-    float zz = 0.f;
+    float acc[N] = {}, zz = 0.f;
     int n = 0;
-    for (int t = lo + wave; t < hi; t += kLossWaves) {
-      if (g.mask && !g.mask[t]) continue;
-      f32x2 l[NC];
+    for (int t = lo + wave * kTokens + group; t - group < hi; t += 2 * kTurn)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = load_pair<T>(g.logits, t * g.ld, c * 128 + lane * 2, g.E);
-      Scores<NC> o;
-      scores<NC>(l, g.score == kScoreSigmoid, o);
+      for (int a = 0; a < 2; ++a) {
+        load(t + (a + 1) * kTurn, row[1 - a], live[1 - a]);
+        if (!live[a]) continue;
+        float v[N];
+        row[a].values(v);
+        Scores<N, Sigmoid> o;
+        o.template of<L>(v);
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] += o.p[c] * o.inv;
-      zz += o.lse * o.lse;
-      ++n;
+        for (int i = 0; i < N; ++i) acc[i] += o.p(i) * o.inv;
+        zz += o.lse * o.lse;
+        ++n;
+      }
+    // the wave's tokens of each turn
+    if constexpr (L < 32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc[i] = swap16(acc[i], false) + swap16(acc[i], true);
+      zz = swap16(zz, false) + swap16(zz, true);
+      n += __shfl_xor(n, 16, 64);
     }
+    if constexpr (L < 64) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) sums[wave][c * 64 + lane] = acc[c];
+      for (int i = 0; i < N; ++i) acc[i] = swap32(acc[i], false) + swap32(acc[i], true);
+      zz = swap32(zz, false) + swap32(zz, true);
+      n += __shfl_xor(n, 32, 64);
+    }
+    if (group == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) sums[wave][i * L + l] = acc[i];
     if (lane == 0) {
       zsum[wave] = zz;
       tokens[wave] = n;
     }
     __syncthreads();
-    float* const out = g.part + (int64_t)(blockIdx.x + s) * loss_row(g.E);
-    for (int e = threadIdx.x; e < g.E; e += kLossWaves * 64) {
-      float v = sums[0][e >> 1][e & 1];
+    float* const out = alone ? g.probs + (int64_t)s * g.E : g.part + (int64_t)(blockIdx.x + s) * loss_row(g.E);
+    int32_t* const out_counts = alone ? g.counts + (int64_t)s * g.E : reinterpret_cast<int32_t*>(out) + g.E;
+    double dot = 0.;
+    for (int o = threadIdx.x; o < L * N; o += kLossThreads) {
+      const int e = column_of<L>(o % L, o / L);
+      if (e >= g.E) continue;
+      float v = sums[0][o];
 #pragma unroll
-      for (int w = 1; w < kLossWaves; ++w) v += sums[w][e >> 1][e & 1];
+      for (int w = 1; w < kLossWaves; ++w) v += sums[w][o];
       out[e] = v;
-      out[g.E + e] = __int_as_float(counts[e]);
+      out_counts[e] = counts[e];
+      dot += (double)counts[e] * v;
+    }
+    if (alone) {
+      dot = wave_sum_f64(dot);
+      if (lane == 0) dots[wave] = dot;
+      __syncthreads();
     }
     if (threadIdx.x == 0) {
       float v = zsum[0];
@@ -191,247 +332,311 @@ __global__ void __launch_bounds__(kLossWaves * 64) router_loss_kernel(RouterLoss
         v += zsum[w];
         m += tokens[w];
       }
-      out[2 * g.E] = v;
-      out[2 * g.E + 1] = __int_as_float(m);
+      if (alone) {
+        for (int w = 1; w < kLossWaves; ++w) dot += dots[w];
+        finish_loss(g, s, dot, v, m);
+      } else {
+        out[2 * g.E] = v;
+        reinterpret_cast<int32_t*>(out)[2 * g.E + 1] = m;
+      }
     }
     __syncthreads();
   }
 }
 
-// The rows of `part` of sequence s: [first, first + rows).
-__device__ __forceinline__ void loss_rows(const RouterLossArgs& g, int s, int64_t& first, int& rows) {
-  const int lo = seq_at(g, s), hi = seq_at(g, s + 1), B = g.tokens_of_block;
-  first = lo / B + s;
-  rows = hi > lo ? (hi - 1) / B - lo / B + 1 : 0;
-}
-
-// 32 columns of a sequence: probs and counts.
-__global__ void __launch_bounds__(256) router_loss_columns_kernel(RouterLossArgs g) {
-  __shared__ float sums[8][32];
-  __shared__ int32_t counts[8][32];
-  const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
+// 32 columns of a sequence: probs and counts, and their products' sum.  The last
+// workgroup of a sequence adds these up, in the columns' order, and the pieces' sums of
+// lse^2: the same bits whichever comes last.
+constexpr int kColumnRows = 16;
+__global__ void __launch_bounds__(32 * kColumnRows) router_loss_columns_kernel(RouterLossArgs g) {
+  __shared__ float sums[kColumnRows][32];
+  __shared__ int32_t counts[kColumnRows][32];
+  __shared__ bool last;
+  const int c = threadIdx.x & 31, r0 = threadIdx.x >> 5, e = blockIdx.x * 32 + c, lane = threadIdx.x & 63;
   const int64_t W = loss_row(g.E);
   for (int s = blockIdx.y; s < g.S; s += gridDim.y) {
-    int64_t first;
-    int rows;
-    loss_rows(g, s, first, rows);
-    const float* const p = g.part + first * W;
+    const int lo = seq_at(g, s), hi = seq_at(g, s + 1), B = g.tokens_of_block;
+    const int rows = hi > lo ? (hi - 1) / B - lo / B + 1 : 0;
+    const float* const p = g.part + (lo / B + (int64_t)s) * W;
     float v = 0.f;
     int n = 0;
-    if (e < g.E) {
-      v = column_sum(p + e, W, r0, rows);
-      for (int r = r0; r < rows; r += 8) n += __float_as_int(p[r * W + g.E + e]);
-    }
+    if (e < g.E)
+      for (int r = r0; r < rows; r += 4 * kColumnRows) {  // four rows in flight
+        float a[4];
+        int b[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = r + u * kColumnRows < rows ? r + u * kColumnRows : r;
+          a[u] = p[at * W + e];
+          b[u] = __float_as_int(p[at * W + g.E + e]);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (r + u * kColumnRows < rows) {
+            v += a[u];
+            n += b[u];
+          }
+      }
     sums[r0][c] = v;
     counts[r0][c] = n;
     __syncthreads();
-    if (r0 == 0 && e < g.E) {
+    if (threadIdx.x < 64) {
+      double dot = 0.;
+      if (r0 == 0 && e < g.E) {
 #pragma unroll
-      for (int i = 1; i < 8; ++i) {
-        v += sums[i][c];
-        n += counts[i][c];
+        for (int i = 1; i < kColumnRows; ++i) {
+          v += sums[i][c];
+          n += counts[i][c];
+        }
+        g.probs[(int64_t)s * g.E + e] = v;
+        g.counts[(int64_t)s * g.E + e] = n;
+        dot = (double)n * v;
       }
-      g.probs[(int64_t)s * g.E + e] = v;
-      g.counts[(int64_t)s * g.E + e] = n;
+      dot = wave_sum_f64(dot);
+      if (lane == 0) {
+        g.dots[(int64_t)s * gridDim.x + blockIdx.x] = dot;
+        __threadfence();
+        last = __hip_atomic_fetch_add(&g.tickets[s], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        __threadfence();
+      }
+    }
+    __syncthreads();
+    if (last && threadIdx.x < 64) {
+      double dot = 0., zz = 0.;
+      int m = 0;
+      if (lane < (int)gridDim.x)  // E / 32 <= 32 of them
+        dot = __hip_atomic_load(&g.dots[(int64_t)s * gridDim.x + lane], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      for (int r = lane; r < rows; r += 64) {
+        zz += p[r * W + 2 * g.E];
+        m += __float_as_int(p[r * W + 2 * g.E + 1]);
+      }
+      dot = wave_sum_f64(dot);
+      zz = wave_sum_f64(zz);
+#pragma unroll
+      for (int d = 32; d; d >>= 1) m += __shfl_xor(m, d, 64);
+      if (lane == 0) finish_loss(g, s, dot, zz, m);
     }
     __syncthreads();
   }
 }
 
-// The losses of a sequence, a wave each: E products and the pieces' sums of lse^2.
-__global__ void __launch_bounds__(64) router_loss_finish_kernel(RouterLossArgs g) {
-  const int lane = threadIdx.x;
-  const int64_t W = loss_row(g.E);
-  for (int s = blockIdx.x; s < g.S; s += gridDim.x) {
-    int64_t first;
-    int rows;
-    loss_rows(g, s, first, rows);
-    double dot = 0., zz = 0.;
-    int n = 0;
-    for (int e = lane; e < g.E; e += 64)
-      dot += (double)g.counts[(int64_t)s * g.E + e] * g.probs[(int64_t)s * g.E + e];
-    for (int r = lane; r < rows; r += 64) {
-      const float* const p = g.part + (first + r) * W + 2 * g.E;
-      zz += p[0];
-      n += __float_as_int(p[1]);
-    }
-    dot = wave_sum_f64(dot);
-    zz = wave_sum_f64(zz);
-#pragma unroll
-    for (int d = 32; d; d >>= 1) n += __shfl_xor(n, d, 64);
-    if (lane == 0) {
-      const double m = n > 0 ? n : 1;
-      g.tokens[s] = n;
-      g.balance[s] = (float)(dot * g.E / (g.k * m * m));
-      g.z[s] = (float)(zz / m);
-    }
-  }
-}
+constexpr int kBackWaves = 4, kBackGroups = 4 * 4 * 256;  // waves of a workgroup; of a launch: four a SIMD
 
-template <typename TO>
-__device__ __forceinline__ void store_pair(void* p, int64_t at, int j, int E, f32x2 v, bool accumulate) {
-  if (j >= E) return;
-  const bool two = j + 1 < E;
-  if constexpr (TO::kType == kF32) {
-    float* const q = static_cast<float*>(p) + at + j;
-    if (two) {
-      if (accumulate) v += *reinterpret_cast<const f32x2_word*>(q);
-      *reinterpret_cast<f32x2_word*>(q) = v;
-    } else {
-      *q = accumulate ? v[0] + *q : v[0];
-    }
+// Four counts from column j on, zeros past the last.
+__device__ __forceinline__ f32x4 load4_counts(const int32_t* p, int j, int E) {
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+  typedef i32x4 __attribute__((aligned(4))) i32x4_word;
+  i32x4 c = {};
+  if (j + 4 <= E) {
+    c = *reinterpret_cast<const i32x4_word*>(p + j);
   } else {
-    uint16_t* const q = static_cast<uint16_t*>(p) + at + j;
-    if (two) {
-      if (accumulate) {
-        const uint32_t h = *reinterpret_cast<const u32_half*>(q);
-        v += f32x2{TO::to_f32((uint16_t)h), TO::to_f32((uint16_t)(h >> 16))};
-      }
-      *reinterpret_cast<u32_half*>(q) = (uint32_t)TO::from_f32(v[0]) | ((uint32_t)TO::from_f32(v[1]) << 16);
-    } else {
-      *q = TO::from_f32(accumulate ? v[0] + TO::to_f32(*q) : v[0]);
-    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (j + r < E) c[r] = p[j + r];
   }
+  return f32x4{(float)c[0], (float)c[1], (float)c[2], (float)c[3]};
 }
 
-constexpr int kBackWaves = 4;
-
-// A wave takes neighbouring tokens: its sequence's coefficients change rarely.
-template <typename T, typename TO, int NC>
-__global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(RouterLossArgs g, int per_wave) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t w0 = ((int64_t)blockIdx.x * kBackWaves + wave) * per_wave;
-  if (w0 >= g.T) return;
-  const int t0 = (int)w0, t1 = g.T - t0 < per_wave ? g.T : t0 + per_wave;
+// The L lanes of a token take neighbouring tokens one after the other: their sequence's
+// coefficients change rarely.
+template <typename T, typename TO, int L, int N, bool Sigmoid>
+__global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(RouterLossArgs g, int per_group) {
+  __shared__ float rows[kBackWaves * 64 / L][L * N];
+  const int lane = threadIdx.x & 63, l = lane % L;
+  float* const chosen = rows[threadIdx.x / L];  // of this token's lanes alone
+  if (g.gates)
+#pragma unroll
+    for (int i = 0; i < N; ++i) chosen[i * L + l] = 0.f;
+  __builtin_amdgcn_wave_barrier();
+  const int64_t first = ((int64_t)blockIdx.x * (kBackWaves * 64) + threadIdx.x) / L * per_group;
+  if (first >= g.T) return;
+  const int t0 = (int)first, t1 = g.T - t0 < per_group ? g.T : t0 + per_group;
   int lo = 0, hi = 0;  // the tokens that the coefficients are of
-  f32x2 coef[NC] = {};
-  float zc = 0.f;
-  for (int t = t0; t < t1; ++t) {
+  float coef[N], zc = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) coef[i] = 0.f;
+  struct Token {
+    Row<T, L, N> row;
+    bool live;
+    int id;
+    float gate, dg;  // lane j of the token: choice j (k <= 16 <= L)
+  };
+  const auto load = [&](int t, Token& o) {
+    if (g.dbalance || g.dz) o.row.load(g.logits, t * g.ld, l, g.E);
+    o.live = !g.mask || g.mask[t];
+    o.id = -1;
+    o.gate = o.dg = 0.f;
+    if (g.gates && l < g.k) {
+      const int64_t at = (int64_t)t * g.k + l;
+      o.id = g.idx[at];
+      o.gate = g.gates[at];
+      o.dg = g.dgates[at];
+    }
+  };
+  const auto token = [&](int t, Token& in) {
     if (t < lo || t >= hi) {
-      const int s = seq_of(g, t);
-      if (s >= g.S) return;  // behind the last sequence
-      lo = seq_at(g, s);
-      hi = seq_at(g, s + 1);
+      const int s = seq_of<L>(g, t, l);
+      lo = s < g.S ? seq_at(g, s) : 0x7FFFFFFF;
+      hi = s < g.S ? seq_at(g, s + 1) : 0x7FFFFFFF;
       if (t >= lo) {
         const int n = g.tokens_in ? g.tokens_in[s] : 1;
         const double m = n > 0 ? n : 1;
         const float f = g.dbalance ? (float)(g.dbalance[s] * ((double)g.E / (g.k * m * m))) : 0.f;
         zc = g.dz ? (float)(2. * g.dz[s] / m) : 0.f;
+        if (g.dbalance) {
+          const int32_t* const q = g.counts_in + (int64_t)s * g.E;
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
+          for (int i = 0; i < N; i += 4) {
+            const f32x4 c = load4_counts(q, column_of<L>(l, i), g.E);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int e = c * 128 + lane * 2 + i;
-            coef[c][i] = g.dbalance && e < g.E ? f * (float)g.counts_in[(int64_t)s * g.E + e] : 0.f;
+            for (int r = 0; r < 4; ++r) coef[i + r] = f * c[r];
           }
+        }
       }
     }
-    if (t < lo) continue;  // before the first sequence
-    const bool live = !g.mask || g.mask[t];
-    if (!live) {
-      if (!g.accumulate)
+    if (t < lo) return;  // in no sequence
+    float d[N];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) store_pair<TO>(g.dlogits, t * g.ldd, c * 128 + lane * 2, g.E, f32x2{}, false);
-      continue;
+    for (int i = 0; i < N; ++i) d[i] = 0.f;
+    if (!in.live) {
+      if (!g.accumulate) store_row<TO, L>(g.dlogits, t * g.ldd, l, g.E, d, false);
+      return;
     }
-    f32x2 d[NC] = {};
     if (g.dbalance || g.dz) {
-      f32x2 l[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) l[c] = load_pair<T>(g.logits, t * g.ld, c * 128 + lane * 2, g.E);
-      Scores<NC> o;
-      scores<NC>(l, g.score == kScoreSigmoid, o);
+      float v[N];
+      in.row.values(v);
+      Scores<N, Sigmoid> o;
+      o.template of<L>(v);
       float along = 0.f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          o.p[c][i] *= o.inv;
-          along += o.p[c][i] * coef[c][i];
-        }
-      along = wave_sum_f32(along);
+      for (int i = 0; i < N; ++i) along += o.p(i) * coef[i];
+      along = lanes_sum<L>(along) * o.inv;
       const float zt = zc * o.lse * o.soft_inv;
+      if (!o.far) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+        for (int i = 0; i < N; ++i) {
+          const float b = o.p(i) * o.inv * (coef[i] - along);
+          d[i] = (Sigmoid ? b * o.down[i] : b) + zt * o.e[i];
+        }
+      } else if constexpr (Sigmoid) {  // rare: the logits are taken from the row again, not kept for it
+        in.row.forget();
+        in.row.values(v);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          d[c][i] = o.p[c][i] * (coef[c][i] - along) * o.down[c][i] + zt * o.soft[c][i];
-    }
-    if (g.gates) {
-      const bool mine = lane < g.k;
-      const int64_t at = (int64_t)t * g.k + (mine ? lane : 0);
-      const int id = g.idx[at];
-      const float gate = mine ? g.gates[at] : 0.f, dg = mine ? g.dgates[at] : 0.f;
-      const float v = gate * (dg - wave_sum_f32(gate * dg));
-      for (int j = 0; j < g.k; ++j) {
-        const int e = __builtin_amdgcn_readlane(id, j);
-        const float add = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), j));
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (e == c * 128 + lane * 2 + i) d[c][i] += add;
+        for (int i = 0; i < N; ++i)
+          d[i] = o.p(i) * o.inv * (coef[i] - along) * (v[i] > kFar ? exp_f32(-v[i]) : o.down[i]) + zt * exp_f32(v[i] - o.top);
       }
     }
+    if (g.gates) {
+      // through a row of zeros in LDS; choices of the same expert all write their sum
+      const float own = in.gate * (in.dg - lanes_sum<L>(in.gate * in.dg));
+      float add = 0.f;
+      for (int j = 0; j < g.k; ++j) {
+        const int e = __shfl(in.id, j, L);
+        const float v = __shfl(own, j, L);
+        if (e == in.id) add += v;
+      }
+      const bool ok = in.id >= 0 && in.id < g.E;
+      if (ok) chosen[in.id] = add;
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int c = 0; c < NC; ++c) store_pair<TO>(g.dlogits, t * g.ldd, c * 128 + lane * 2, g.E, d[c], g.accumulate);
+      for (int i = 0; i < N; i += 4) {
+        const f32x4 c = *reinterpret_cast<const f32x4*>(chosen + column_of<L>(l, i));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) d[i + r] += c[r];
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (ok) chosen[in.id] = 0.f;
+    }
+    store_row<TO, L>(g.dlogits, t * g.ldd, l, g.E, d, g.accumulate);
+  };
+  Token a, b;
+  load(t0, a);
+  for (int t = t0; t < t1; t += 2) {
+    load(t + 1 < t1 ? t + 1 : t, b);
+    token(t, a);
+    if (t + 1 >= t1) break;
+    load(t + 2 < t1 ? t + 2 : t, a);
+    token(t + 1, b);
   }
 }
 
 int block_tokens(int T) {
-  const int b = (T + kLossBlocks - 1) / kLossBlocks;
-  return b < kLossWaves ? kLossWaves : b;
+  const int b = (T + kLossBlocks - 1) / kLossBlocks, turn = kLossWaves * 4;
+  return b < turn ? turn : (b + turn - 1) / turn * turn;
+}
+bool loss_alone(const RouterLossArgs& a) { return a.T <= kAloneTokens && a.S <= kAloneSequences; }
+
+// Lanes of a token and elements of a lane.
+template <typename F>
+void by_experts(int E, const F& run) {
+  if (E <= 64) run(IntC<16>{}, IntC<4>{});
+  else if (E <= 128) run(IntC<16>{}, IntC<8>{});
+  else if (E <= 256) run(IntC<32>{}, IntC<8>{});
+  else if (E <= 384) run(IntC<32>{}, IntC<12>{});
+  else if (E <= 512) run(IntC<32>{}, IntC<16>{});
+  else if (E <= 768) run(IntC<64>{}, IntC<12>{});
+  else run(IntC<64>{}, IntC<16>{});
 }
 
-template <typename F>
-void by_columns(int E, const F& run) {
-  if (E <= 128) run(IntC<1>{});
-  else if (E <= 256) run(IntC<2>{});
-  else if (E <= 384) run(IntC<3>{});
-  else if (E <= 512) run(IntC<4>{});
-  else if (E <= 768) run(IntC<6>{});
-  else run(IntC<8>{});
+// The workspace: the pieces' rows, the columns' sums of products, the tickets.
+struct LossWs {
+  size_t dots, tickets, total;
+};
+LossWs loss_ws(const RouterLossArgs& a) {
+  LossWs w{};
+  if (loss_alone(a)) return w;
+  const int B = block_tokens(a.T), blocks = (a.T + B - 1) / B;
+  const size_t rows = ((size_t)blocks + a.S) * loss_row(a.E) * 4;
+  w.dots = (rows + 255) / 256 * 256;
+  w.tickets = w.dots + (size_t)a.S * ((a.E + 31) / 32) * 8;
+  w.total = w.tickets + (size_t)a.S * 4;
+  return w;
 }
 
 }  // namespace
 
-size_t router_loss_workspace(const RouterLossArgs& a) {
-  const int B = block_tokens(a.T);
-  return ((size_t)(a.T + B - 1) / B + a.S) * loss_row(a.E) * 4;
-}
+size_t router_loss_workspace(const RouterLossArgs& a) { return loss_ws(a).total; }
 
-hipError_t launch_router_loss(RouterLossArgs a, hipStream_t stream) {
-  a.tokens_of_block = block_tokens(a.T);
-  const unsigned blocks = (a.T + a.tokens_of_block - 1) / a.tokens_of_block;
-  if (blocks)
-    by_columns(a.E, [&](auto nc) {
-      constexpr int NC = decltype(nc)::value;
-      const auto run = [&](auto k) { hipLaunchKernelGGL(k, dim3(blocks), dim3(kLossWaves * 64), 0, stream, a); };
-      if (a.type == kF32) run(router_loss_kernel<F32, NC>);
-      else if (a.type == kBf16) run(router_loss_kernel<Bf16, NC>);
-      else run(router_loss_kernel<F16, NC>);
-    });
-  const unsigned most = a.S < 4096 ? a.S : 4096;
-  hipLaunchKernelGGL(router_loss_columns_kernel, dim3((a.E + 31) / 32, most), dim3(256), 0, stream, a);
-  hipLaunchKernelGGL(router_loss_finish_kernel, dim3(most), dim3(64), 0, stream, a);
+hipError_t launch_router_loss(RouterLossArgs a, void* ws, hipStream_t stream) {
+  const bool alone = loss_alone(a);
+  a.tokens_of_block = alone ? kAloneTokens : block_tokens(a.T);
+  const LossWs w = loss_ws(a);
+  a.part = static_cast<float*>(ws);
+  a.dots = reinterpret_cast<double*>(static_cast<char*>(ws) + w.dots);
+  a.tickets = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + w.tickets);
+  const unsigned blocks = a.T > a.tokens_of_block ? (a.T + a.tokens_of_block - 1) / a.tokens_of_block : 1;
+  by_experts(a.E, [&](auto lanes, auto elements) {
+    constexpr int L = decltype(lanes)::value, N = decltype(elements)::value;
+    const auto run = [&](auto k) { hipLaunchKernelGGL(k, dim3(blocks), dim3(kLossThreads), 0, stream, a, alone); };
+    const auto scored = [&](auto t) {
+      using T = decltype(t);
+      a.score == kScoreSigmoid ? run(router_loss_kernel<T, L, N, true>) : run(router_loss_kernel<T, L, N, false>);
+    };
+    a.type == kF32 ? scored(F32{}) : a.type == kBf16 ? scored(Bf16{}) : scored(F16{});
+  });
+  if (!alone)
+    hipLaunchKernelGGL(router_loss_columns_kernel, dim3((a.E + 31) / 32, a.S < 4096 ? a.S : 4096), dim3(32 * kColumnRows), 0,
+                       stream, a);
   return hipGetLastError();
 }
 
 hipError_t launch_router_loss_backward(RouterLossArgs a, hipStream_t stream) {
   if (!a.T) return hipSuccess;
-  int per_wave = (a.T + 8191) / 8192;  // eight waves a SIMD
-  const unsigned blocks = (unsigned)(((int64_t)a.T + kBackWaves * per_wave - 1) / (kBackWaves * per_wave));
-  by_columns(a.E, [&](auto nc) {
-    constexpr int NC = decltype(nc)::value;
-    const auto run = [&](auto k) { hipLaunchKernelGGL(k, dim3(blocks), dim3(kBackWaves * 64), 0, stream, a, per_wave); };
-    if (a.type == kF32)
-      a.out_type == kF32 ? run(router_loss_backward_kernel<F32, F32, NC>)
-                         : a.out_type == kBf16 ? run(router_loss_backward_kernel<F32, Bf16, NC>)
-                                               : run(router_loss_backward_kernel<F32, F16, NC>);
-    else if (a.type == kBf16)
-      a.out_type == kF32 ? run(router_loss_backward_kernel<Bf16, F32, NC>) : run(router_loss_backward_kernel<Bf16, Bf16, NC>);
-    else
-      a.out_type == kF32 ? run(router_loss_backward_kernel<F16, F32, NC>) : run(router_loss_backward_kernel<F16, F16, NC>);
+  by_experts(a.E, [&](auto lanes, auto elements) {
+    constexpr int L = decltype(lanes)::value, N = decltype(elements)::value;
+    const int64_t groups = kBackGroups * (64 / L);
+    const int per = (int)((a.T + groups - 1) / groups), tokens = kBackWaves * 64 / L * per;
+    const unsigned blocks = (unsigned)((a.T + tokens - 1) / tokens);
+    const auto run = [&](auto k) { hipLaunchKernelGGL(k, dim3(blocks), dim3(kBackWaves * 64), 0, stream, a, per); };
+    const auto scored = [&](auto t, auto to) {
+      using T = decltype(t);
+      using TO = decltype(to);
+      a.score == kScoreSigmoid ? run(router_loss_backward_kernel<T, TO, L, N, true>)
+                               : run(router_loss_backward_kernel<T, TO, L, N, false>);
+    };
+    if (a.type == kF32) a.out_type == kF32 ? scored(F32{}, F32{}) : a.out_type == kBf16 ? scored(F32{}, Bf16{}) : scored(F32{}, F16{});
+    else if (a.type == kBf16) a.out_type == kF32 ? scored(Bf16{}, F32{}) : scored(Bf16{}, Bf16{});
+    else a.out_type == kF32 ? scored(F16{}, F32{}) : scored(F16{}, F16{});
   });
   return hipGetLastError();
 }

@@ -2,8 +2,6 @@
 both scores, expert counts from one to the most, ragged and empty sequences,
 masks, masked experts, dropped and repeated choices, strides, and the gradients against
 differences."""
-import math
-
 import pytest
 import torch
 
@@ -28,8 +26,10 @@ def scores64(l, sigmoid):
     """p, 1 - sigmoid (or 1), lse, softmax, and relative bounds of p, lse's absolute one.
 
     An exponential of l - m: the difference and the product with log2 e are rounded and
-    log2 e is itself, 3 half steps of the exponent; the instruction adds a step.  A row's
-    sum has 2 ceil(E / 128) + 8 additions; reciprocal and product 2 steps."""
+    log2 e is itself, 3 half steps of the exponent; the instruction adds a step.  For the
+    softmax m is the row's largest; with sigmoids it may be 0, and |l - m| is below |l| +
+    (largest - l) either way.  A row's sum has at most 24 + 6 additions; reciprocal and
+    product 2 steps."""
     E = l.shape[1]
     m = l.amax(1, keepdim=True)
     m = torch.where(torch.isinf(m), torch.zeros_like(m), m)
@@ -37,8 +37,10 @@ def scores64(l, sigmoid):
     s = e.sum(1, keepdim=True)
     inv = torch.where(s > 0, 1 / s, torch.zeros_like(s))
     soft = e * inv
-    adds = 2 * math.ceil(E / 128) + 8
+    adds = 30
     far = torch.where(torch.isinf(l), torch.zeros_like(l), m - l)
+    if sigmoid:
+        far = far + torch.where(torch.isinf(l), torch.zeros_like(l), l.abs())
     r_e = 3 * H32 * far + U32
     r_s = (r_e * soft).sum(1, keepdim=True) + adds * U32
     r_soft = r_e + r_s + 2 * U32
@@ -51,10 +53,12 @@ def scores64(l, sigmoid):
     u = torch.exp(ls - torch.where(torch.isinf(ls.amax(1, keepdim=True)), torch.zeros_like(m), ls.amax(1, keepdim=True)))
     su = u.sum(1, keepdim=True)
     p = torch.where(su > 0, u / su, torch.zeros_like(u))
-    a = torch.where(torch.isinf(l), torch.zeros_like(l), l.abs())
-    r_u = 3 * H32 * (a + far) + 5 * U32  # e^-|l| (or e^(l - m)), 1 + it, the reciprocal, their product
+    # 1 / (1 + e e^m), off by what e and e^m are (|m| <= |l| where m < 0), the product, the sum and
+    # the reciprocal by a step each; its product with e once more
+    r_down = 3 * H32 * far + 5 * U32
+    r_u = r_e + r_down + U32
     r_p = r_u + (r_u * p).sum(1, keepdim=True) + (adds + 2) * U32
-    return p, torch.sigmoid(-l), lse, soft, r_soft, r_p, 3 * H32 * a + 5 * U32, e_lse
+    return p, torch.sigmoid(-l), lse, soft, r_soft, r_p, r_down, e_lse
 
 
 def cuts_of(seqs, T):
@@ -102,7 +106,7 @@ def backward64(logits, idx, loss, dbalance, dz, gates, dgates, sigmoid, seqs, ma
     live = torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
     p, down, lse, soft, r_soft, r_p, r_down, e_lse = scores64(torch.where(live[:, None], l, torch.zeros_like(l)), sigmoid)
     d, e = torch.full_like(l, float("nan")), torch.zeros_like(l)
-    adds = 2 * math.ceil(E / 128) + 8
+    adds = 30
     for s, (lo, hi) in enumerate(cuts_of(seqs, T)):
         if lo >= hi:
             continue
