@@ -70,7 +70,12 @@ struct Row {
 #pragma unroll
     for (int c = 0; c < N / 4; ++c) {
       const int j = (c * L + l) * 4;
-      if constexpr (T::kType == kF32) {
+      if (E == L * N) {  // every lane's are there
+        if constexpr (T::kType == kF32)
+          raw[c] = __builtin_bit_cast(Words, *reinterpret_cast<const f32x4_word*>(static_cast<const float*>(p) + row + j));
+        else
+          raw[c] = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(p) + row + j);
+      } else if constexpr (T::kType == kF32) {
         const float* const q = static_cast<const float*>(p) + row + j;
         if (j + 4 <= E) {
           raw[c] = __builtin_bit_cast(Words, *reinterpret_cast<const f32x4_word*>(q));
@@ -109,9 +114,13 @@ template <typename TO, int L, int N>
 __device__ __forceinline__ void store_row(void* p, int64_t row, int l, int E, const float (&d)[N], bool accumulate) {
 #pragma unroll
   for (int c = 0; c < N / 4; ++c) {
-    const int j = (c * L + l) * 4, n = E - j < 4 ? E - j : 4;
-    if (n <= 0) continue;
+    const int j = (c * L + l) * 4, n = E == L * N || E - j >= 4 ? 4 : E - j;
     f32x4 v = {d[c * 4], d[c * 4 + 1], d[c * 4 + 2], d[c * 4 + 3]};
+    if (E == L * N && !accumulate) {
+      store4_from_f32(p, row + j, 4, TO::kType, true, v);
+      continue;
+    }
+    if (n <= 0) continue;
     if (accumulate) v += load4_as_f32(p, row + j, n, TO::kType, n == 4);
     store4_from_f32(p, row + j, n, TO::kType, n == 4, v);
   }
@@ -151,12 +160,15 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// A token's scores, p times a common factor: softmax e = exp(l - m), m the row's largest logit.
+// A token's scores, p times a common factor.  Exponents are taken to base 2: with M = m log2 e
+// rounded once, e = 2^(l log2 e - M) is one multiply-add and one instruction, and M's rounding is in
+// all of a row's alike.
 //
-// Sigmoids: m = min(largest, 0), e = exp(min(l, 60) - m) and down = 1 / (1 + e e^m): p = e down is
-// sigmoid(l) e^-m, which keeps its digits where all logits are far below 0, and down is 1 - sigmoid(l),
-// from one exponential and one reciprocal.  From 60 on the sigmoid is 1 in fp32; where a row has such
-// logits (`far`) 1 - sigmoid is e^-l there, and the softmax of the z loss takes exponentials of its own.
+// Softmax: e = exp(l - m), m the row's largest logit; p = e.
+// Sigmoids: m = min(largest, 0), down = 1 / (1 + e 2^M) and p = e down: p is sigmoid(l) e^-m, which
+// keeps its digits where all logits are far below 0, and down is 1 - sigmoid(l), from one exponential
+// and one reciprocal.  Rows with a logit past 60 (`far`, there the sigmoid is 1 in fp32) take e of
+// min(l, 60) for it, and 1 - sigmoid and the softmax of the z loss from exponentials of their own.
 //
 // A row of -inf alone has no probabilities: its sums are 0, and so are their reciprocals and
 // its lse.
@@ -173,28 +185,34 @@ struct Scores {
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, l[i]);
     top = lanes_max<L>(top);
-    float m = top == -INFINITY ? 0.f : top, soft_sum = 0.f, sum = 0.f;
+    float m = top == -INFINITY ? 0.f : Sigmoid ? fminf(top, 0.f) : top, soft_sum = 0.f, sum = 0.f;
+    const float M = m * kLog2e;
     far = Sigmoid && !(top <= kFar);  // NaN too
-    if constexpr (Sigmoid) m = fminf(m, 0.f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      e[i] = exp_f32((Sigmoid ? (l[i] > kFar ? kFar : l[i]) : l[i]) - m);
-      soft_sum += e[i];
+    for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f(l[i] * kLog2e - M);
+    if (!(fabsf(m) <= 1e30f)) {  // M may pass fp32: a row of the type's lowest value
+#pragma unroll
+      for (int i = 0; i < N; ++i) e[i] = exp_f32(l[i] - m);
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) soft_sum += e[i];
     if constexpr (Sigmoid) {
-      const float f = exp_f32(m);
+      if (far) {
+        soft_sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          soft_sum += exp_f32(l[i] - top);
+          if (l[i] > kFar) e[i] = __builtin_amdgcn_exp2f(kFar * kLog2e);
+        }
+      }
+      const float f = __builtin_amdgcn_exp2f(M);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         down[i] = __builtin_amdgcn_rcpf(1.0f + e[i] * f);
         sum += e[i] * down[i];
       }
       sum = lanes_sum<L>(sum);
-      if (far) {
-        soft_sum = 0.f;
-        m = top;
-#pragma unroll
-        for (int i = 0; i < N; ++i) soft_sum += exp_f32(l[i] - top);
-      }
+      if (far) m = top;
     }
     soft_sum = lanes_sum<L>(soft_sum);
     soft_inv = soft_sum == 0.f ? 0.f : __builtin_amdgcn_rcpf(soft_sum);
@@ -515,8 +533,9 @@ __global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(R
       if (!o.far) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float b = o.p(i) * o.inv * (coef[i] - along);
-          d[i] = (Sigmoid ? b * o.down[i] : b) + zt * o.e[i];
+          const float t = (coef[i] - along) * o.inv;
+          if constexpr (Sigmoid) d[i] = o.e[i] * (o.down[i] * (o.down[i] * t) + zt);
+          else d[i] = o.e[i] * (t + zt);
         }
       } else if constexpr (Sigmoid) {  // rare: the logits are taken from the row again, not kept for it
         in.row.forget();
