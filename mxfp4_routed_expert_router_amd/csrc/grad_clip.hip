@@ -49,71 +49,98 @@ bool next_table(const moe_fp4_grad_tensor* t, int n, int* at, GradTable& g) {
 }
 unsigned table_blocks(const GradTable& g) { return g.chunks < kGradBlocks ? g.chunks : kGradBlocks; }
 
-// The tensor of chunk c, and its elements [lo, lo + n) of it.
-__device__ __forceinline__ const GradEntry& chunk_of(const GradTable& g, int c, int64_t& lo, int& n) {
+constexpr int kThreads = 256, kLoads = kChunk / 16 / kThreads;  // 16-byte loads of a thread and chunk
+
+// A workgroup takes every gridDim.x-th chunk (neighbouring ones took 8% longer: the memory
+// then has 2048 places open at a time) and searches for the tensor of its first one only.
+// A thread takes the 16 bytes at 16 (256 u + thread) of a chunk.
+struct Chunk {
+  const char* in;
+  int64_t at;  // first element
+  int n;       // elements
+  int entry;
+};
+__device__ __forceinline__ int entry_of(const GradTable& g, int c) {
   int a = 0, b = g.n - 1;
   while (a < b) {
     const int mid = (a + b + 1) >> 1;
     if (g.e[mid].first <= c) a = mid;
     else b = mid - 1;
   }
-  const GradEntry& e = g.e[a];
-  const int per = kChunk / (e.type == kF32 ? 4 : 2);
-  lo = (int64_t)(c - e.first) * per;
-  n = e.n - lo < per ? (int)(e.n - lo) : per;
-  return e;
+  return a;
 }
-
-constexpr int kLoads = kChunk / 16 / 256;  // 16-byte loads of a thread and chunk
+__device__ __forceinline__ Chunk chunk_at(const GradTable& g, int c, int entry) {
+  const GradEntry& e = g.e[entry];
+  const int size = e.type == kF32 ? 4 : 2, per = kChunk / size;
+  Chunk o;
+  o.at = (int64_t)(c - e.first) * per;
+  o.n = e.n - o.at < per ? (int)(e.n - o.at) : per;
+  o.in = static_cast<const char*>(e.in) + o.at * size;
+  o.entry = entry;
+  return o;
+}
+// The thread's bytes, zeros past the chunk's end.
+__device__ __forceinline__ void load_chunk(const GradTable& g, const Chunk& c, u32x4 (&v)[kLoads]) {
+  const bool wide = g.e[c.entry].type == kF32;
+  const int bytes = c.n * (wide ? 4 : 2);
+  if (bytes == kChunk) {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) v[u] = *reinterpret_cast<const u32x4_any*>(c.in + (u * kThreads + threadIdx.x) * 16);
+    return;
+  }
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int o = (u * kThreads + threadIdx.x) * 16;
+    v[u] = zero4();
+    if (o + 16 <= bytes) {
+      v[u] = *reinterpret_cast<const u32x4_any*>(c.in + o);
+    } else if (o < bytes) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (wide) {
+          if (o + 4 * i < bytes) v[u][i] = *reinterpret_cast<const uint32_t*>(c.in + o + 4 * i);
+        } else {
+          const uint16_t* const q = reinterpret_cast<const uint16_t*>(c.in + o + 4 * i);
+          if (o + 4 * i < bytes) v[u][i] = q[0];
+          if (o + 4 * i + 2 < bytes) v[u][i] |= (uint32_t)q[1] << 16;
+        }
+    }
+  }
+}
+// Element r of 16 bytes.
+template <typename T>
+__device__ __forceinline__ float element(const u32x4& v, int r) {
+  if constexpr (T::kType == kF32) return __uint_as_float(v[r]);
+  else return T::to_f32((uint16_t)(v[r / 2] >> (16 * (r & 1))));
+}
 
 template <typename T>
-__device__ __forceinline__ double squares_of_chunk(const void* p, int64_t lo, int n) {
+__device__ __forceinline__ void add_squares(const u32x4 (&v)[kLoads], double (&s)[2]) {
   constexpr int V = T::kType == kF32 ? 4 : 8;
-  double s[2] = {0., 0.};
-  const int i0 = threadIdx.x * V;
-  if (n == kLoads * 256 * V) {
-    u32x4 v[kLoads];
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      v[u] = *reinterpret_cast<const u32x4_any*>(static_cast<const char*>(p) + (lo + i0 + u * 256 * V) * (16 / V));
+  for (int u = 0; u < kLoads; ++u)
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-#pragma unroll
-      for (int r = 0; r < V; ++r) {
-        float f;
-        if constexpr (T::kType == kF32) f = __uint_as_float(v[u][r]);
-        else f = T::to_f32((uint16_t)(v[u][r / 2] >> (16 * (r & 1))));
-        const double d = f;
-        s[r & 1] += d * d;
-      }
-  } else {
-    for (int i = i0; i < n; i += 256 * V)
-#pragma unroll
-      for (int r = 0; r < V; ++r)
-        if (i + r < n) {
-          float f;
-          if constexpr (T::kType == kF32) f = static_cast<const float*>(p)[lo + i + r];
-          else f = T::to_f32(static_cast<const uint16_t*>(p)[lo + i + r]);
-          const double d = f;
-          s[r & 1] += d * d;
-        }
-  }
-  return s[0] + s[1];
+    for (int r = 0; r < V; ++r) {
+      const double d = element<T>(v[u], r);
+      s[r & 1] += d * d;
+    }
 }
 
-__global__ void __launch_bounds__(256) grad_sumsq_kernel(GradTable g, double* part) {
-  __shared__ double of_wave[4];
-  double s = 0.;
+__global__ void __launch_bounds__(kThreads, 6) grad_sumsq_kernel(GradTable g, double* part) {
+  __shared__ double of_wave[kThreads / 64];
+  double s[2] = {0., 0.};
+  int entry = entry_of(g, blockIdx.x);
   for (int c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-    int64_t lo;
-    int n;
-    const GradEntry& e = chunk_of(g, c, lo, n);
-    if (e.type == kF32) s += squares_of_chunk<F32>(e.in, lo, n);
-    else if (e.type == kBf16) s += squares_of_chunk<Bf16>(e.in, lo, n);
-    else s += squares_of_chunk<F16>(e.in, lo, n);
+    while (entry + 1 < g.n && g.e[entry + 1].first <= c) ++entry;
+    const int type = g.e[entry].type;
+    u32x4 v[kLoads];
+    load_chunk(g, chunk_at(g, c, entry), v);
+    if (type == kF32) add_squares<F32>(v, s);
+    else if (type == kBf16) add_squares<Bf16>(v, s);
+    else add_squares<F16>(v, s);
   }
-  s = wave_sum_f64(s);
-  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = s;
+  const double sum = wave_sum_f64(s[0] + s[1]);
+  if ((threadIdx.x & 63) == 0) of_wave[threadIdx.x >> 6] = sum;
   __syncthreads();
   if (threadIdx.x == 0) part[blockIdx.x] = ((of_wave[0] + of_wave[1]) + of_wave[2]) + of_wave[3];
 }
@@ -132,70 +159,65 @@ __global__ void __launch_bounds__(1024) grad_sumsq_finish_kernel(const double* p
 
 // The product is rounded to fp32, and for a 16-bit result once more.
 template <typename T, typename TO>
-__device__ __forceinline__ void chunk_clip(const void* p, void* out, int64_t lo, int n, float factor) {
+__device__ __forceinline__ void scale_chunk(const GradTable& g, const Chunk& c, const u32x4 (&v)[kLoads], float factor) {
   constexpr int V = T::kType == kF32 ? 4 : 8;
-  const int i0 = threadIdx.x * V;
-  const auto one = [&](int i) {
-    float f;
-    if constexpr (T::kType == kF32) f = static_cast<const float*>(p)[lo + i];
-    else f = T::to_f32(static_cast<const uint16_t*>(p)[lo + i]);
-    f *= factor;
-    if constexpr (TO::kType == kF32) static_cast<float*>(out)[lo + i] = f;
-    else static_cast<uint16_t*>(out)[lo + i] = TO::from_f32(f);
-  };
-  if (n == kLoads * 256 * V) {
-    u32x4 v[kLoads];
+  char* const out = static_cast<char*>(g.e[c.entry].out) + c.at * (TO::kType == kF32 ? 4 : 2);
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-      v[u] = *reinterpret_cast<const u32x4_any*>(static_cast<const char*>(p) + (lo + i0 + u * 256 * V) * (16 / V));
+  for (int u = 0; u < kLoads; ++u) {
+    const int i = (u * kThreads + threadIdx.x) * V;
+    if (i >= c.n) break;
+    float f[V];
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      float f[V];
+    for (int r = 0; r < V; ++r) f[r] = element<T>(v[u], r) * factor;
+    const bool whole = i + V <= c.n;
+    if constexpr (TO::kType == kF32) {
+      float* const q = reinterpret_cast<float*>(out) + i;
+      if (whole) *reinterpret_cast<f32x4_word*>(q) = f32x4{f[0], f[1], f[2], f[3]};
+      else
 #pragma unroll
-      for (int r = 0; r < V; ++r) {
-        if constexpr (T::kType == kF32) f[r] = __uint_as_float(v[u][r]);
-        else f[r] = T::to_f32((uint16_t)(v[u][r / 2] >> (16 * (r & 1))));
-        f[r] *= factor;
-      }
-      const int64_t at = lo + i0 + u * 256 * V;
-      if constexpr (TO::kType == kF32) {
-        *reinterpret_cast<f32x4_word*>(static_cast<float*>(out) + at) = f32x4{f[0], f[1], f[2], f[3]};
+        for (int r = 0; r < V; ++r)
+          if (i + r < c.n) q[r] = f[r];
+    } else {
+      uint32_t h[V / 2];
+#pragma unroll
+      for (int r = 0; r < V / 2; ++r)
+        h[r] = (uint32_t)TO::from_f32(f[2 * r]) | ((uint32_t)TO::from_f32(f[2 * r + 1]) << 16);
+      uint16_t* const q = reinterpret_cast<uint16_t*>(out) + i;
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < V; ++r)
+          if (i + r < c.n) q[r] = (uint16_t)(h[r / 2] >> (16 * (r & 1)));
+      } else if constexpr (V == 4) {
+        *reinterpret_cast<u32x2_any*>(q) = u32x2{h[0], h[1]};
       } else {
-        uint32_t h[V / 2];
-#pragma unroll
-        for (int r = 0; r < V / 2; ++r)
-          h[r] = (uint32_t)TO::from_f32(f[2 * r]) | ((uint32_t)TO::from_f32(f[2 * r + 1]) << 16);
-        uint16_t* const q = static_cast<uint16_t*>(out) + at;
-        if constexpr (V == 4) *reinterpret_cast<u32x2_any*>(q) = u32x2{h[0], h[1]};
-        else *reinterpret_cast<u32x4_any*>(q) = u32x4{h[0], h[1], h[2], h[3]};
+        *reinterpret_cast<u32x4_any*>(q) = u32x4{h[0], h[1], h[2], h[3]};
       }
     }
-  } else {
-    for (int i = i0; i < n; i += 256 * V)
-#pragma unroll
-      for (int r = 0; r < V; ++r)
-        if (i + r < n) one(i + r);
   }
 }
 
-__global__ void __launch_bounds__(256) grad_clip_kernel(GradTable g, const double* sumsq, float max_norm, float eps,
-                                                        float* norm) {
+// The chunks go backwards: the last ones that the norm read are still in the 256 MB cache.
+__global__ void __launch_bounds__(kThreads, 6) grad_clip_kernel(GradTable g, const double* sumsq, float max_norm, float eps,
+                                                             float* norm) {
   const double root = sqrt(*sumsq), most = (double)max_norm / (root + (double)eps);
   const float factor = (float)(most > 1. ? 1. : most);  // NaN stays NaN
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
-  for (int c = blockIdx.x; c < g.chunks; c += gridDim.x) {
-    int64_t lo;
-    int n;
-    const GradEntry& e = chunk_of(g, c, lo, n);
+  int entry = g.n ? entry_of(g, g.chunks - 1 - (int)blockIdx.x) : 0;
+  for (int c = g.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+    while (g.e[entry].first > c) --entry;
+    const GradEntry& e = g.e[entry];
     if (factor == 1.f && e.in == e.out) continue;
+    const Chunk chunk = chunk_at(g, c, entry);
+    u32x4 v[kLoads];
+    load_chunk(g, chunk, v);
     if (e.type == kF32) {
-      if (e.out_type == kF32) chunk_clip<F32, F32>(e.in, e.out, lo, n, factor);
-      else if (e.out_type == kBf16) chunk_clip<F32, Bf16>(e.in, e.out, lo, n, factor);
-      else chunk_clip<F32, F16>(e.in, e.out, lo, n, factor);
+      if (e.out_type == kF32) scale_chunk<F32, F32>(g, chunk, v, factor);
+      else if (e.out_type == kBf16) scale_chunk<F32, Bf16>(g, chunk, v, factor);
+      else scale_chunk<F32, F16>(g, chunk, v, factor);
     } else if (e.type == kBf16) {
-      chunk_clip<Bf16, Bf16>(e.in, e.out, lo, n, factor);
+      scale_chunk<Bf16, Bf16>(g, chunk, v, factor);
     } else {
-      chunk_clip<F16, F16>(e.in, e.out, lo, n, factor);
+      scale_chunk<F16, F16>(g, chunk, v, factor);
     }
   }
 }
@@ -215,7 +237,7 @@ hipError_t launch_grad_sumsq(const moe_fp4_grad_tensor* t, int n, double* sumsq,
   int parts = 0;
   GradTable g;
   for (int at = 0; next_table(t, n, &at, g); parts += table_blocks(g))
-    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(table_blocks(g)), dim3(256), 0, stream, g, part + parts);
+    hipLaunchKernelGGL(grad_sumsq_kernel, dim3(table_blocks(g)), dim3(kThreads), 0, stream, g, part + parts);
   hipLaunchKernelGGL(grad_sumsq_finish_kernel, dim3(1), dim3(1024), 0, stream, part, parts, sumsq, accumulate);
   return hipGetLastError();
 }
@@ -225,11 +247,11 @@ hipError_t launch_grad_clip(const moe_fp4_grad_tensor* t, int n, const double* s
   GradTable g;
   bool first = true;
   for (int at = 0; next_table(t, n, &at, g); first = false)
-    hipLaunchKernelGGL(grad_clip_kernel, dim3(table_blocks(g)), dim3(256), 0, stream, g, sumsq, max_norm, eps,
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(table_blocks(g)), dim3(kThreads), 0, stream, g, sumsq, max_norm, eps,
                        first ? norm : nullptr);
   if (first) {  // no elements: the norm alone
     g.n = g.chunks = 0;
-    hipLaunchKernelGGL(grad_clip_kernel, dim3(1), dim3(256), 0, stream, g, sumsq, max_norm, eps, norm);
+    hipLaunchKernelGGL(grad_clip_kernel, dim3(1), dim3(kThreads), 0, stream, g, sumsq, max_norm, eps, norm);
   }
   return hipGetLastError();
 }

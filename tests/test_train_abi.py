@@ -21,7 +21,7 @@ def lib():
 
 
 def loss_dims(b, **over):
-    d = dict(T=100, E=16, k=4, S=3, score=0, type=1, out_type=1, ld=0, ldd=0)
+    d = dict(T=1000, E=16, k=4, S=3, score=0, type=1, out_type=1, ld=0, ldd=0)
     d.update(over)
     return b.RouterLossDims(**d)
 
@@ -76,6 +76,7 @@ def test_loss_pointers(b, lib):
     assert forward(lib, d, ws=None, n=n.value) == lib.EINVAL
     assert forward(lib, d, ws=FAKE + 64, n=n.value) == lib.EALIGN
     assert forward(lib, loss_dims(b, S=1), seqs=None) == lib.EWORKSPACE  # one sequence needs no offsets
+    assert lib._lib.moe_fp4_router_loss_workspace_size(ctypes.byref(loss_dims(b, T=100)), ctypes.byref(n)) == 0 and n.value == 0
     for null in ("logits", "tokens", "counts", "seqs", "out", "idx", "gates", "dgates"):
         assert backward(lib, d, flags=0, **{null: None}) == lib.EINVAL
     assert backward(lib, d, flags=0, db=None, dz=None, gates=None, dgates=None) == lib.EINVAL
