@@ -16,7 +16,7 @@ SOURCES = ["api.hip", "route.hip", "router.hip", "decode.hip", "prefill.hip", "p
            "api_block.hip", "product.hip", "product_fwd.hip", "product_dgrad.hip",
            "product_wgrad.hip", "product_few.hip", "product_row.hip",
            "slope.hip", "norm.hip", "norm_backward.hip",
-           "api_train.hip", "router_loss.hip", "grad_clip.hip", "api_w4.hip", "w4.hip", "w4_row.hip", "w4_hold.hip"]
+           "api_train.hip", "router_loss.hip", "grad_clip.hip", "api_w4.hip", "w4.hip", "w4_row.hip", "w4_hold.hip", "w4_wide.hip"]
 
 # Packed fp32 VALU ops are switched off for all device code (the host pass warns
 # that it does not know the feature; that is harmless).

@@ -21,6 +21,12 @@ struct W4Args {
 };
 void launch_w4_row(const W4Args& a, hipStream_t stream);  // one or two rows
 void launch_w4_hold(const W4Args& a, hipStream_t stream); // up to 16 rows; MX, int4 groups of 128 and 256
+// Any rows, where the scales and zeros of a column are at most kWideRowBytes.
+constexpr int kWideRowBytes = 160;
+inline int w4_row_bytes(const W4Args& a) {
+  return a.groups * ((a.code == kMx ? 1 : a.scale_type == kF32 ? 4 : 2) + (a.zeros ? 1 : 0));
+}
+void launch_w4_wide(const W4Args& a, hipStream_t stream);
 hipError_t launch_w4(const W4Args& a, hipStream_t stream);
 
 }  // namespace moe_fp4

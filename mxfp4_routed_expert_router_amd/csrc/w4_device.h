@@ -8,6 +8,7 @@ namespace moe_fp4 {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t __attribute__((aligned(1))) u32_byte;
+typedef u32x4 __attribute__((aligned(1))) u32x4_byte;
 
 // The two codes of byte `byte` (a constant where the call is unrolled) as 16-bit values.
 template <typename T>
