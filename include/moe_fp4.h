@@ -520,7 +520,7 @@ int moe_fp4_norm_backward(const moe_fp4_norm_dims *dims, const void *dy, const v
  * Logits l [T][E], the chosen experts idx [T][k] (moe_fp4_route's topk_idx) and the
  * batch's sequences: sequence s is the tokens seqs[s] .. seqs[s+1]-1 (int32 [S+1] on
  * the device, ascending; NULL with S = 1: all tokens).  mask [T] (bytes, NULL: none)
- * leaves out tokens whose byte is 0: nothing of them is read but the byte.  With n the
+ * leaves out tokens whose byte is 0: whatever else they hold does not count.  With n the
  * sequence's tokens that are left and p a token's probabilities,
  *   SOFTMAX  p = softmax(l)        SIGMOID  p_e = sigmoid(l_e) / sum_i sigmoid(l_i)
  *   counts[s][e] = its choices of expert e          tokens[s] = n
@@ -580,7 +580,7 @@ int moe_fp4_router_loss_backward(const moe_fp4_router_loss_dims *dims, const voi
 
 /* ---- the gradients' global norm, and clipping
  *   sumsq = sum over all tensors' elements of g^2           (fp64)
- *   norm  = sqrt(sumsq)      factor = min(1, max_norm / (norm + eps))
+ *   norm  = sqrt(sumsq)      factor = min(1, max_norm / (norm + eps))  (1 where norm + eps = 0)
  *   out   = g * factor
  * in two calls, so that ranks that hold parts of the gradients can add up sumsq between
  * them.  Squares are taken and summed in fp64: no gradient of the three types is lost

@@ -172,7 +172,7 @@ __device__ __forceinline__ void scale_chunk(const GradTable& g, const Chunk& c, 
     const bool whole = i + V <= c.n;
     if constexpr (TO::kType == kF32) {
       float* const q = reinterpret_cast<float*>(out) + i;
-      if (whole) *reinterpret_cast<f32x4_word*>(q) = f32x4{f[0], f[1], f[2], f[3]};
+      if (whole) __builtin_nontemporal_store(f32x4{f[0], f[1], f[2], f[3]}, reinterpret_cast<f32x4_word*>(q));
       else
 #pragma unroll
         for (int r = 0; r < V; ++r)
@@ -188,9 +188,9 @@ __device__ __forceinline__ void scale_chunk(const GradTable& g, const Chunk& c, 
         for (int r = 0; r < V; ++r)
           if (i + r < c.n) q[r] = (uint16_t)(h[r / 2] >> (16 * (r & 1)));
       } else if constexpr (V == 4) {
-        *reinterpret_cast<u32x2_any*>(q) = u32x2{h[0], h[1]};
+        __builtin_nontemporal_store(u32x2{h[0], h[1]}, reinterpret_cast<u32x2_any*>(q));
       } else {
-        *reinterpret_cast<u32x4_any*>(q) = u32x4{h[0], h[1], h[2], h[3]};
+        __builtin_nontemporal_store(u32x4{h[0], h[1], h[2], h[3]}, reinterpret_cast<u32x4_any*>(q));
       }
     }
   }
@@ -199,7 +199,7 @@ __device__ __forceinline__ void scale_chunk(const GradTable& g, const Chunk& c, 
 // The chunks go backwards: the last ones that the norm read are still in the 256 MB cache.
 __global__ void __launch_bounds__(kThreads, 6) grad_clip_kernel(GradTable g, const double* sumsq, float max_norm, float eps,
                                                              float* norm) {
-  const double root = sqrt(*sumsq), most = (double)max_norm / (root + (double)eps);
+  const double root = sqrt(*sumsq), over = root + (double)eps, most = over == 0. ? 1. : (double)max_norm / over;
   const float factor = (float)(most > 1. ? 1. : most);  // NaN stays NaN
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
   int entry = g.n ? entry_of(g, g.chunks - 1 - (int)blockIdx.x) : 0;

@@ -211,7 +211,7 @@ void launch_tiles(const W4Args& a, hipStream_t stream) {
 //   64 rows   N = 288: 1 1 8 8.5, 2 2 4 12.8; 5120 x 5120: 30.4, 22.5, 4 4 4 30.4; 9216 x 5120: 54.0, 34.9, 31.4
 template <typename T, int Code, int Group>
 void launch_rows(const W4Args& a, hipStream_t stream) {
-  if (a.N <= 512) launch_tiles<T, Code, Group, 1, 1, 8>(a, stream);
+  if (a.N <= 512 && a.M <= 16384) launch_tiles<T, Code, Group, 1, 1, 8>(a, stream);  // (a grid's rows end at 65535)
   else if (a.M <= 16) {
     // two columns' tiles where that fills the CUs about once, or many times
     if ((a.N > 4096 && a.N <= 8192) || a.N >= 16384) launch_tiles<T, Code, Group, 2, 1, 8>(a, stream);

@@ -131,7 +131,8 @@ def test_accumulate_and_no_tensors(moe):
     # a norm of zero divides by eps, or by nothing
     z = torch.zeros(10, device="cuda")
     for eps in (1e-6, 0.0):
-        assert moe.moe_fp4_grad_clip([z], ss, 1.0, eps=eps).item() == 0 and not bool(z.any())
+        for max_norm in (1.0, 0.0):
+            assert moe.moe_fp4_grad_clip([z], ss, max_norm, eps=eps).item() == 0 and bool((z == 0).all())
 
 
 def test_more_than_2_to_32_bytes(moe):

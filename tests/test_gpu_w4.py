@@ -242,6 +242,18 @@ def test_no_rows_and_refusals(moe):
         moe.moe_fp4_linear_w4(x, moe.W4Weights(odd, w.scales))
 
 
+def test_most_rows(moe):
+    """2^20 rows: more than a grid's second dimension holds of single tiles."""
+    g = gen(11)
+    M, N, K = 1 << 20, 17, 64
+    w, w64, mag = weights(moe, g, N, K, KINDS[0])
+    x = randn(g, M, K, dtype=BF)
+    y = moe.moe_fp4_linear_w4(x, w, out_dtype=F32)
+    tail = slice(M - 200, M)
+    bounded(y[tail], x[tail].double() @ w64.t(), (K + 16) * U32 * (x[tail].double().abs() @ mag.t()), F32, "last rows")
+    assert torch.equal(y[:40], moe.moe_fp4_linear_w4(x[:40], w, out_dtype=F32))
+
+
 def test_codes_past_32_bits(moe):
     """65536 rows 128 KB apart: byte offsets past 2^32."""
     N, K = 65536, 64
