@@ -233,9 +233,9 @@ void launch_type(const W4Args& a, hipStream_t stream) {
 // Where each kernel is taken, by time (one MI355X, bf16 x, weights cold, us):
 //   rows as a stream of the weights, one and two from K = 1024 on: one row of 9216 x 5120 8.0, on
 //     the matrix cores 13.2; two 11.4, 13.2; four 17.0, 13.4; one of 5120 x 512 3.7, 3.1
-//   up to 16 rows of many columns held in registers, where a wave's scales fit beside them:
-//     16 rows, MX, 9216 x 5120: tiles 19.5, held 15.3 (3 rows 13.4, 14.6); 16384 x 5120 19.0 held;
-//     65536 x 5120: 74, 54
+//   up to 16 rows of many columns held in registers, where a wave's scales fit beside them (tiles,
+//     held): 16 rows, MX, 9216 x 5120: 19.4, 15.3; 3 rows 13.4, 14.6; 8192 x 8192: 16.8 by tiles,
+//     whose workgroups are 256 there; 16384 x 5120: 19.0 held; 65536 x 5120: 74, 54
 //   shared through LDS (tiles, shared): 8 rows, int4 groups of 64, 32768 x 5120: 38, 47; 65536 x
 //     5120: 75, 54; 32 rows, MX, 24576 x 5120: 40, 45; 65536 x 5120: 101, 56; 64 rows, 16384 x 5120:
 //     34, 50; 24576 x 5120: 61, 52; 65536 x 5120: 127, 63
@@ -243,7 +243,7 @@ hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
   const bool hold = a.code == kMx || a.group >= 128;
   const int wide = a.M > 32 ? 20480 : a.M > 16 ? 32768 : 49152;  // columns from which rows are shared
   if (a.M <= 2 && a.K >= 1024) launch_w4_row(a, stream);
-  else if (a.M <= 16 && a.N >= 16384 && hold) launch_w4_hold(a, stream);
+  else if (a.M <= 16 && hold && a.N >= (a.M > 8 ? 8193 : 16384)) launch_w4_hold(a, stream);
   else if (a.N >= wide && w4_row_bytes(a) <= kWideRowBytes) launch_w4_wide(a, stream);
   else if (a.type == kBf16) launch_type<Bf16>(a, stream);
   else launch_type<F16>(a, stream);

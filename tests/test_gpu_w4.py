@@ -130,7 +130,7 @@ def test_scales_at_their_ends(moe, dt):
 @pytest.mark.parametrize("M,N,K", [(3, 16384, 32), (16, 16385, 96), (7, 16400, 1184), (16, 20001, 2080), (5, 65536, 160),
                                    (11, 16384, 4992), (4, 16389, 5152), (16, 16384, 10336), (40, 20500, 96),
                                    (64, 20485, 5120), (70, 20480, 1184), (33, 20481, 640), (20, 32769, 160), (32, 32800, 2336),
-                                   (16, 49153, 416), (3, 49160, 1024), (100, 20480, 32)])
+                                   (16, 49153, 416), (3, 49160, 1024), (9, 8193, 288), (16, 9216, 5120), (100, 20480, 32)])
 def test_many_columns(moe, M, N, K, kind, dt):
     """Wide weights, whose short last tile overlaps the one before; sums of one to three
     chunks; rows shared through LDS."""
