@@ -11,9 +11,14 @@
 //
 // Both passes read the logits once.  L lanes (32 from 129 to 512 experts) take a token, 64 / L
 // tokens a wave: a row's maximum and sums are then a few exchanges between neighbouring
-// lanes for several tokens at once (with a wave a token they and the exponentials took
-// more time than the bytes).  A lane keeps the same columns for every token: the sums
+// lanes for several tokens at once (with a wave a token the longest backward pass took
+// 76 us, 34 now; with 16 lanes 51, for its registers).  A lane keeps the same columns for every token: the sums
 // over tokens stay in registers, and so do the coefficients c of the backward pass.
+//
+// One MI355X: forward, 16384 tokens of 384 experts in fp32, 25 MB, 11.2 us and 8.9 for the
+// columns (both chains of loads that wait for one another: offsets, rows, pieces); 64 tokens
+// 5.5 us.  Backward 14.1 us (50 MB, 3.6 TB/s); 65536 tokens, sigmoid, bf16, 34 us for 101 MB, of which
+// the vector units are busy 59 %: about 25 instructions an element.
 #include "block_device.h"
 #include "router_loss.h"
 

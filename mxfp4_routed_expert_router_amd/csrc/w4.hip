@@ -11,6 +11,9 @@
 // The next unit's loads are on their way while one is computed.  The waves' sums meet in
 // LDS and are added in wave order.
 //
+// 16 rows of 5120 x 9216, int4: 16.5 us where the weights' 24 MB take 5: 160 workgroups read
+// 47 MB of x from the L2 besides, and a wave's nine units follow one another.
+//
 // MX with bf16 x: the conversion from E2M1 takes the scale and its result is exact in
 // bf16, so that the products of all groups run into one sum.  Elsewhere (fp16 does not
 // hold all scales, a scaled int4 is not exact in 16 bits) a scale's inputs have a sum of

@@ -10,6 +10,9 @@
 // a lane's sums are of one column, whose scale it can apply, and a product takes one
 // group.  The waves' sums of a tile meet in LDS and are added in wave order.  A sum longer
 // than the eight waves hold is taken in chunks, the tiles' totals kept in LDS between them.
+//
+// 16 rows of 65536 x 5120, MX: 53 us for 178 MB.  A CU has one workgroup, 80 KB of codes on
+// their way; its tiles wait for one another at their barriers.
 #include "w4_device.h"
 
 namespace moe_fp4 {
