@@ -443,7 +443,11 @@ __global__ void __launch_bounds__(32 * kColumnRows) router_loss_columns_kernel(R
   }
 }
 
-constexpr int kBackWaves = 4, kBackGroups = 4 * 4 * 256;  // waves of a workgroup; of a launch: four a SIMD
+constexpr int kBackWaves = 4;  // of a workgroup
+// Waves that a SIMD holds by the registers that they need, and so many a launch has (of 65536
+// tokens' bf16 logits with sigmoids, 34 us with four, 47 with three for one register too many).
+template <typename T, int N, bool Sigmoid>
+constexpr int kBackOfSimd = !Sigmoid ? 4 : T::kType == kF32 ? (N <= 12 ? 3 : 2) : N <= 12 ? 4 : 3;
 
 // Four counts from column j on, zeros past the last.
 __device__ __forceinline__ f32x4 load4_counts(const int32_t* p, int j, int E) {
@@ -463,7 +467,7 @@ __device__ __forceinline__ f32x4 load4_counts(const int32_t* p, int j, int E) {
 // The L lanes of a token take neighbouring tokens one after the other: their sequence's
 // coefficients change rarely.
 template <typename T, typename TO, int L, int N, bool Sigmoid>
-__global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(RouterLossArgs g, int per_group) {
+__global__ void __launch_bounds__(kBackWaves * 64, kBackOfSimd<T, N, Sigmoid>) router_loss_backward_kernel(RouterLossArgs g, int per_group) {
   __shared__ float rows[kBackWaves * 64 / L][L * N];
   const int lane = threadIdx.x & 63, l = lane % L;
   float* const chosen = rows[threadIdx.x / L];  // of this token's lanes alone
@@ -648,15 +652,15 @@ hipError_t launch_router_loss_backward(RouterLossArgs a, hipStream_t stream) {
   if (!a.T) return hipSuccess;
   by_experts(a.E, [&](auto lanes, auto elements) {
     constexpr int L = decltype(lanes)::value, N = decltype(elements)::value;
-    const int64_t groups = kBackGroups * (64 / L);
-    const int per = (int)((a.T + groups - 1) / groups), tokens = kBackWaves * 64 / L * per;
-    const unsigned blocks = (unsigned)((a.T + tokens - 1) / tokens);
-    const auto run = [&](auto k) { hipLaunchKernelGGL(k, dim3(blocks), dim3(kBackWaves * 64), 0, stream, a, per); };
+    const auto run = [&](auto k, int of_simd) {
+      const int groups = of_simd * 4 * 256 * (64 / L), per = (a.T + groups - 1) / groups, tokens = kBackWaves * 64 / L * per;
+      hipLaunchKernelGGL(k, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kBackWaves * 64), 0, stream, a, per);
+    };
     const auto scored = [&](auto t, auto to) {
       using T = decltype(t);
       using TO = decltype(to);
-      a.score == kScoreSigmoid ? run(router_loss_backward_kernel<T, TO, L, N, true>)
-                               : run(router_loss_backward_kernel<T, TO, L, N, false>);
+      a.score == kScoreSigmoid ? run(router_loss_backward_kernel<T, TO, L, N, true>, kBackOfSimd<T, N, true>)
+                               : run(router_loss_backward_kernel<T, TO, L, N, false>, kBackOfSimd<T, N, false>);
     };
     if (a.type == kF32) a.out_type == kF32 ? scored(F32{}, F32{}) : a.out_type == kBf16 ? scored(F32{}, Bf16{}) : scored(F32{}, F16{});
     else if (a.type == kBf16) a.out_type == kF32 ? scored(Bf16{}, F32{}) : scored(Bf16{}, Bf16{});
