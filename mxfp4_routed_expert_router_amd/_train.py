@@ -99,7 +99,7 @@ def moe_fp4_router_loss(logits: torch.Tensor, topk_idx: torch.Tensor, score: int
     ws, nws, keep = _workspace(_lib.moe_fp4_router_loss_workspace_size, d, workspace=workspace, device=dev)
     # one allocation for the five results
     counts, tokens, probs, balance, z = torch.empty(S * (2 * E + 3), dtype=torch.float32, device=dev).split(
-        (S * E, S, S * E, S, S)) if S > 0 else [logits.new_empty(0)] * 5
+        (S * E, S, S * E, S, S))
     counts, tokens, probs = counts.view(torch.int32).view(-1, E), tokens.view(torch.int32), probs.view(-1, E)
     _call(_lib.moe_fp4_router_loss, dev, d, logits.data_ptr(), topk_idx.data_ptr(), _opt(seqs), _opt(mask),
           counts.data_ptr(), tokens.data_ptr(), probs.data_ptr(), balance.data_ptr(), z.data_ptr(), ws, nws)
