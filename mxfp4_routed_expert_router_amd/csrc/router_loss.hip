@@ -444,10 +444,11 @@ __global__ void __launch_bounds__(32 * kColumnRows) router_loss_columns_kernel(R
 }
 
 constexpr int kBackWaves = 4;  // of a workgroup
-// Waves that a SIMD holds by the registers that they need, and so many a launch has (of 65536
-// tokens' bf16 logits with sigmoids, 34 us with four, 47 with three for one register too many).
+// Waves that a SIMD holds by the registers that they take, and so many a launch has.  (Of 65536
+// tokens' bf16 logits with sigmoids, at 128 registers and four waves 34 us; 47 with one
+// register more, and 43 where the compiler is told to keep to four, for the order it then takes.)
 template <typename T, int N, bool Sigmoid>
-constexpr int kBackOfSimd = !Sigmoid ? 4 : T::kType == kF32 ? (N <= 12 ? 3 : 2) : N <= 12 ? 4 : 3;
+constexpr int kBackOfSimd = !Sigmoid || (T::kType != kF32 && N <= 12) ? 4 : 3;
 
 // Four counts from column j on, zeros past the last.
 __device__ __forceinline__ f32x4 load4_counts(const int32_t* p, int j, int E) {
@@ -467,7 +468,7 @@ __device__ __forceinline__ f32x4 load4_counts(const int32_t* p, int j, int E) {
 // The L lanes of a token take neighbouring tokens one after the other: their sequence's
 // coefficients change rarely.
 template <typename T, typename TO, int L, int N, bool Sigmoid>
-__global__ void __launch_bounds__(kBackWaves * 64, kBackOfSimd<T, N, Sigmoid>) router_loss_backward_kernel(RouterLossArgs g, int per_group) {
+__global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(RouterLossArgs g, int per_group) {
   __shared__ float rows[kBackWaves * 64 / L][L * N];
   const int lane = threadIdx.x & 63, l = lane % L;
   float* const chosen = rows[threadIdx.x / L];  // of this token's lanes alone
