@@ -522,7 +522,10 @@ __global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(R
         }
       }
     }
-    if (t < lo) return;  // in no sequence
+    if (t < lo) {  // in no sequence; the next token may be the first of this one, whose coefficients it loads
+      hi = lo;
+      return;
+    }
     float d[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) d[i] = 0.f;

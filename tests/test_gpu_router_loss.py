@@ -449,3 +449,57 @@ def test_binding_refusals(moe):
         moe.moe_fp4_router_loss_backward(logits, idx, r, dz=torch.ones(2, device="cuda"))
     with pytest.raises(TypeError):
         moe.moe_fp4_router_loss_backward(logits.to(BF), idx, r, dz=one, out_dtype=HF)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E", [(50001, 100), (30001, 384), (17001, 600)])
+def test_tokens_behind_a_late_first_sequence(moe, T, E, score):
+    """Sequences that start behind tokens of none, several tokens a group of lanes: every token from the
+    first offset on has its gradient, the ones before keep what they held."""
+    sigmoid = score == "sigmoid"
+    g = gen(T)
+    k = 3
+    logits, idx, gates, _, _ = batch(g, T, E, k, 0, F32, False)
+    a, b, dg = randn(g, 3), randn(g, 3), randn(g, T, k)
+    for start in (1, 6, T // 2 + 1):
+        seqs = torch.tensor([start, start + 4000, start + 4000, T - 2], dtype=torch.int32, device="cuda")
+        r = moe.moe_fp4_router_loss(logits, idx, score=int(sigmoid), seqs=seqs)
+        got = torch.full((T, E), 7.0, device="cuda")
+        moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=a, dz=b, gates=gates, dgates=dg, score=int(sigmoid), seqs=seqs,
+                                         dlogits=got)
+        want, e, none = backward64(logits, idx, r, a, b, gates, dg, sigmoid, seqs, None)
+        assert none.nonzero()[:, 0].tolist() == list(range(start)) + [T - 2, T - 1]
+        assert bool((got[none] == 7.0).all())
+        bounded(got[~none], want[~none], e[~none], F32, f"dlogits from {start} on")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradients_past_32_bits(moe, score):
+    """2^20 tokens of 1024 experts at a row stride of 4200, the gradient over the logits: rows at both
+    ends and between, and nothing beside the rows."""
+    sigmoid = score == "sigmoid"
+    T, E = 1 << 20, 1024
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    g = gen(15)
+    buf = torch.empty(T, 4200, dtype=BF, device="cuda").normal_(generator=g)
+    logits = buf[:, :E]
+    idx = (torch.rand(T, 1, generator=g, device="cuda").square() * (E - 1)).to(torch.int32)
+    start, cut = 37, T - 100
+    seqs = torch.tensor([start, cut, T - 9], dtype=torch.int32, device="cuda")
+    r = moe.moe_fp4_router_loss(logits, idx, score=int(sigmoid), seqs=seqs)
+    assert r.tokens.tolist() == [cut - start, T - 9 - cut]
+    rows = torch.cat([torch.arange(a, a + 300, device="cuda") for a in (0, T // 2 - 7, T - 300)])
+    before, beside = logits[rows], buf[:, E:].clone()
+    a, b = torch.tensor([1e6, 1.0], device="cuda"), torch.tensor([1e6, 1.0], device="cuda")
+    moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=a, dz=b, score=int(sigmoid), seqs=seqs, dlogits=logits)
+    assert torch.equal(buf[:, E:], beside)
+    got = logits[rows]
+    none = (rows < start) | (rows >= T - 9)
+    assert torch.equal(got[none], before[none])
+    for s, (lo, hi) in enumerate(((start, cut), (cut, T - 9))):
+        of = (rows >= lo) & (rows < hi)
+        one = moe.RouterLoss(r.counts[s:s + 1], r.tokens[s:s + 1], None, None, None)
+        want, e, _ = backward64(before[of], idx[rows][of], one, a[s:s + 1], b[s:s + 1], None, None, sigmoid, None, None)
+        bounded(got[of], want, e, BF, f"dlogits of sequence {s}")
