@@ -45,7 +45,7 @@ bool next_table(const moe_fp4_grad_tensor* t, int n, int* at, GradTable& g) {
     if (v.n == 0) continue;
     const int64_t c = (v.n + chunk_elements(v.type) - 1) / chunk_elements(v.type);  // 2^27 at most
     if (g.chunks > (1 << 30)) break;
-    g.e[g.n++] = GradEntry{v.data, v.out ? v.out : v.data, v.n, g.chunks, (int16_t)v.type, (int16_t)v.out_type};
+    g.e[g.n++] = GradEntry{v.data, v.out ? v.out : v.data, v.n, g.chunks, (int16_t)v.type, (int16_t)(v.out ? v.out_type : v.type)};
     g.chunks += (int32_t)c;
   }
   return g.n > 0;

@@ -179,3 +179,21 @@ def test_binding_refusals(moe):
         moe.moe_fp4_grad_sumsq([t], accumulate=True)
     with pytest.raises(ValueError):
         moe.moe_fp4_grad_sumsq([t, t.cpu()])
+
+
+@pytest.mark.parametrize("out_type", [1, 2, 3, -1, 1 << 20])
+def test_a_type_of_no_result_is_not_read(moe, out_type):
+    """The C call in place, out_type anything: fp32 tensors are clipped in fp32."""
+    from mxfp4_routed_expert_router_amd import _lib, _train
+    g = gen(6)
+    tensors = [randn(g, 20000), randn(g, 33, dtype=BF), randn(g, 9000)]
+    keep = [t.clone() for t in tensors]
+    ss = moe.moe_fp4_grad_sumsq(tensors)
+    rows = [_train.GradTensor(t.data_ptr(), None, t.numel(), _train._TYPES[t.dtype], out_type) for t in tensors]
+    table = (_train.GradTensor * 3)(*rows)
+    norm = torch.zeros(1, device="cuda")
+    assert _lib._lib.moe_fp4_grad_clip(table, 3, ss.data_ptr(), 1.0, 0.0, norm.data_ptr(),
+                                       torch.cuda.current_stream().cuda_stream) == _lib.OK
+    factor = 1.0 / sumsq64(keep).sqrt().item()
+    for t, k in zip(tensors, keep):
+        bounded(t, k.double() * factor, 1.1 * U32 * k.double().abs() * factor, t.dtype, "clipped")
