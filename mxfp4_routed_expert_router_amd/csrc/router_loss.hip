@@ -167,7 +167,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // A token's scores, p times a common factor.  Exponents are taken to base 2: with M = m log2 e
 // rounded once, e = 2^(l log2 e - M) is one multiply-add and one instruction, and M's rounding is in
-// all of a row's alike.
+// all of a row's alike: a factor within 2^(1/16) up to |m| = 1e6, but past fp32's range from 1e10 on.
+// Rows further out take e = exp(l - m), whose difference is exact wherever e is not 0.
 //
 // Softmax: e = exp(l - m), m the row's largest logit; p = e.
 // Sigmoids: m = min(largest, 0), down = 1 / (1 + e 2^M) and p = e down: p is sigmoid(l) e^-m, which
@@ -195,7 +196,7 @@ struct Scores {
     far = Sigmoid && !(top <= kFar);  // NaN too
 #pragma unroll
     for (int i = 0; i < N; ++i) e[i] = __builtin_amdgcn_exp2f(l[i] * kLog2e - M);
-    if (!(fabsf(m) <= 1e30f)) {  // M may pass fp32: a row of the type's lowest value
+    if (!(fabsf(m) <= 1e6f)) {  // inf too
 #pragma unroll
       for (int i = 0; i < N; ++i) e[i] = exp_f32(l[i] - m);
     }

@@ -503,3 +503,48 @@ def test_gradients_past_32_bits(moe, score):
         one = moe.RouterLoss(r.counts[s:s + 1], r.tokens[s:s + 1], None, None, None)
         want, e, _ = backward64(before[of], idx[rows][of], one, a[s:s + 1], b[s:s + 1], None, None, sigmoid, None, None)
         bounded(got[of], want, e, BF, f"dlogits of sequence {s}")
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [1e5, 1.1e6, 3e7, 1e9, 2e9, 1e10, 3e10, 1e20, 9e29, 2e30, 1e38])
+def test_logits_of_any_magnitude(moe, size, score, dt):
+    """Rows whose largest logits all lie at +-size: alone, or above others that are further down by
+    `size`, whose exponentials are exactly 0.  The largest ones' exponentials are equal, off
+    by a step; a sum of them by 30 additions, reciprocal and products by 6 more steps.  lse is off
+    by that and its own roundings: of m log2 e and of the sum with m."""
+    sigmoid = score == "sigmoid"
+    T, E, k = 4, 70, 2
+    logits = torch.empty(T, E, device="cuda")
+    for t, c in enumerate((size, -size)):
+        logits[2 * t], logits[2 * t + 1] = c, c - size
+        logits[2 * t + 1, 5:12] = c
+    logits = logits.to(dt)
+    idx = torch.tensor([[5, 6]] * T, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, device="cuda")
+    for t in range(T):
+        row, ids = logits[t:t + 1], idx[t:t + 1]
+        l = row.double()
+        soft, lse = torch.softmax(l, 1), torch.logsumexp(l, 1).item()
+        u = torch.nn.functional.logsigmoid(l)
+        p, down = (torch.softmax(u, 1), torch.sigmoid(-l)) if sigmoid else (soft, torch.ones_like(l))
+        r = moe.moe_fp4_router_loss(row, ids, score=int(sigmoid))
+        bounded(r.probs, p, 36 * U32 * p, F32, f"probs {t}")
+        counts = torch.zeros(1, E, dtype=torch.float64, device="cuda")
+        counts[0, 5:7] = 1
+        balance = E / k * (counts * p).sum(1)
+        bounded(r.balance, balance, 37 * U32 * balance, F32, f"balance {t}")
+        e_lse = U32 * (3 * abs(lse) + 44)
+        if lse * lse < 3.3e38:
+            assert abs(r.z.item() - lse * lse) <= 2 * abs(lse) * e_lse + e_lse ** 2 + U32 * lse * lse
+        else:
+            assert r.z.item() == float("inf")
+        c = E / k * counts
+        along = (p * c).sum(1, keepdim=True)
+        d1 = p * (c - along) * down
+        e1 = 80 * U32 * p * (c + along) * down
+        d2 = 2 * lse * soft
+        e2 = (44 * U32 * abs(lse) + e_lse) * 2 * soft
+        for db, dz, want, e in ((one, None, d1, e1), (None, one, d2, e2), (one, one, d1 + d2, e1 + e2)):
+            got = moe.moe_fp4_router_loss_backward(row, ids, r, dbalance=db, dz=dz, score=int(sigmoid), out_dtype=F32)
+            bounded(got, want, e + TINY, F32, f"dlogits {t}")
