@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(R
 #pragma unroll
       for (int i = 0; i < N; ++i) along += o.p(i) * coef[i];
       along = lanes_sum<L>(along) * o.inv;
-      const float zt = zc * o.lse * o.soft_inv;
+      const float zt = !Sigmoid || g.dz ? zc * o.lse * o.soft_inv : 0.f;  // lse of a logit of inf is NaN
       if (!o.far) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -556,7 +556,8 @@ __global__ void __launch_bounds__(kBackWaves * 64) router_loss_backward_kernel(R
         in.row.values(v);
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          d[i] = o.p(i) * o.inv * (coef[i] - along) * (v[i] > kFar ? exp_f32(-v[i]) : o.down[i]) + zt * exp_f32(v[i] - o.top);
+          d[i] = o.p(i) * o.inv * (coef[i] - along) * (v[i] > kFar ? exp_f32(-v[i]) : o.down[i]) +
+                 zt * exp_f32(fminf(v[i] - o.top, 0.f));  // inf - inf counts for zt alone, which is NaN then
       }
     }
     if (g.gates) {

@@ -548,3 +548,28 @@ def test_logits_of_any_magnitude(moe, size, score, dt):
         for db, dz, want, e in ((one, None, d1, e1), (None, one, d2, e2), (one, one, d1 + d2, e1 + e2)):
             got = moe.moe_fp4_router_loss_backward(row, ids, r, dbalance=db, dz=dz, score=int(sigmoid), out_dtype=F32)
             bounded(got, want, e + TINY, F32, f"dlogits {t}")
+
+
+def test_sigmoid_of_an_infinite_logit(moe):
+    """Its probability and the balance loss's gradient are finite: that of its own logit is 0."""
+    g = gen(13)
+    T, E, k = 6, 40, 2
+    logits = randn(g, T, E)
+    logits[0, 4] = logits[1, 0] = logits[1, 1] = logits[3, 39] = float("inf")
+    logits[3, 2], logits[3, 3] = 100.0, float("-inf")
+    idx = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    r = moe.moe_fp4_router_loss(logits, idx, score=moe.SCORE_SIGMOID)
+    s = torch.sigmoid(logits.double())
+    p = s / s.sum(1, keepdim=True)
+    # |l| below 8 or the sigmoid is 1 in fp32 (100: off by 2^-144): the exponent 24 half steps, 40 steps else
+    rel = 64 * U32
+    bounded(r.probs, p.sum(0)[None], (rel + T * U32) * p.sum(0)[None], F32, "probs")
+    one = torch.ones(1, device="cuda")
+    got = moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=one, score=moe.SCORE_SIGMOID)
+    c = E / (k * T * T) * r.counts.double()
+    along = p @ c.t()
+    down = torch.sigmoid(-logits.double())
+    bounded(got, p * (c - along) * down, 2 * rel * p * (c + along) * down + TINY, F32, "dlogits")
+    assert not bool(got[torch.isinf(logits)].any())
+    d = moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=one, dz=one, score=moe.SCORE_SIGMOID)
+    assert (~torch.isfinite(d).all(1)).nonzero()[:, 0].tolist() == [0, 1, 3]
