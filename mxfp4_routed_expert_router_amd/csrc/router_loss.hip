@@ -173,12 +173,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // Softmax: e = exp(l - m), m the row's largest logit; p = e.
 // Sigmoids: m = min(largest, 0), down = 1 / (1 + e 2^M) and p = e down: p is sigmoid(l) e^-m, which
 // keeps its digits where all logits are far below 0, and down is 1 - sigmoid(l), from one exponential
-// and one reciprocal.  Rows with a logit past 60 (`far`, there the sigmoid is 1 in fp32) take e of
-// min(l, 60) for it, and 1 - sigmoid and the softmax of the z loss from exponentials of their own.
+// and one reciprocal.  Rows with a logit past 24 (`far`, there the sigmoid is 1 in fp32) take e of
+// min(l, 24) for it, and 1 - sigmoid and the softmax of the z loss from exponentials of their own:
+// the backward pass multiplies by down twice before it does by e, and down^2 = e^-48 times a
+// coefficient is still a normal number (from e^-80 on it was 0).
 //
 // A row of -inf alone has no probabilities: its sums are 0, and so are their reciprocals and
 // its lse.
-constexpr float kFar = 60.f;
+constexpr float kFar = 24.f;
 template <int N, bool Sigmoid>
 struct Scores {
   float e[N], down[Sigmoid ? N : 1];

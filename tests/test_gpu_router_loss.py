@@ -573,3 +573,18 @@ def test_sigmoid_of_an_infinite_logit(moe):
     assert not bool(got[torch.isinf(logits)].any())
     d = moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=one, dz=one, score=moe.SCORE_SIGMOID)
     assert (~torch.isfinite(d).all(1)).nonzero()[:, 0].tolist() == [0, 1, 3]
+
+
+@pytest.mark.parametrize("E", [33, 384])
+def test_gradients_of_saturated_sigmoids(moe, E):
+    """1 - sigmoid of logits up to 90: e^-l keeps its digits down to the smallest normal numbers."""
+    g = gen(14)
+    T, k = 40, 4
+    logits = (torch.arange(T, device="cuda")[:, None] * 2.25 + randn(g, T, E)).clamp(max=80.0)
+    logits[::4, ::3] -= 30.0
+    idx = torch.topk(logits, k, dim=1).indices.to(torch.int32)
+    r = check_forward(moe, logits, idx, True, None, None)
+    dbal = torch.full((1,), 1000.0, device="cuda")
+    got = moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=dbal, score=moe.SCORE_SIGMOID)
+    want, e, _ = backward64(logits, idx, r, dbal, None, None, None, True, None, None)
+    bounded(got, want, e, F32, "dlogits")
