@@ -202,7 +202,8 @@ __device__ __forceinline__ void scale_chunk(const GradTable& g, const Chunk& c, 
 // The chunks go backwards: the last ones that the norm read are still in the 256 MB cache.
 __global__ void __launch_bounds__(kThreads, 6) grad_clip_kernel(GradTable g, const double* sumsq, float max_norm, float eps,
                                                              float* norm) {
-  const double root = sqrt(*sumsq), over = root + (double)eps, most = over == 0. ? 1. : (double)max_norm / over;
+  const double root = sqrt(*sumsq), over = root + (double)eps;
+  const double most = over == 0. ? 1. : over == INFINITY ? 0. : (double)max_norm / over;  // also where both are inf
   const float factor = (float)(most > 1. ? 1. : most);  // NaN stays NaN
   if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)root;
   int entry = g.n ? entry_of(g, g.chunks - 1 - (int)blockIdx.x) : 0;

@@ -197,3 +197,13 @@ def test_a_type_of_no_result_is_not_read(moe, out_type):
     factor = 1.0 / sumsq64(keep).sqrt().item()
     for t, k in zip(tensors, keep):
         bounded(t, k.double() * factor, 1.1 * U32 * k.double().abs() * factor, t.dtype, "clipped")
+
+
+def test_a_norm_of_inf_without_a_limit(moe):
+    """max_norm inf: nothing is clipped; an infinite norm still gives a factor of 0."""
+    inf = float("inf")
+    t = torch.ones(100, device="cuda")
+    assert moe.moe_fp4_grad_clip([t], moe.moe_fp4_grad_sumsq([t]), inf).item() == 10.0 and bool((t == 1).all())
+    t[5] = inf
+    norm = moe.moe_fp4_grad_clip([t], moe.moe_fp4_grad_sumsq([t]), inf)
+    assert norm.item() == inf and torch.isnan(t).nonzero()[:, 0].tolist() == [5] and bool((t[:5] == 0).all())
