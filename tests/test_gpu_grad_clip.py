@@ -207,3 +207,17 @@ def test_a_norm_of_inf_without_a_limit(moe):
     t[5] = inf
     norm = moe.moe_fp4_grad_clip([t], moe.moe_fp4_grad_sumsq([t]), inf)
     assert norm.item() == inf and torch.isnan(t).nonzero()[:, 0].tolist() == [5] and bool((t[:5] == 0).all())
+
+
+@pytest.mark.parametrize("max_norm", [0.5, 1e9])
+@pytest.mark.parametrize("out", [False, True], ids=["in_place", "out"])
+def test_lists_of_more_chunks_than_workgroups(moe, out, max_norm):
+    """Some 200 MB in one launch: a workgroup goes from tensor to tensor, of other types and of sizes
+    from one element to many times all workgroups' chunks."""
+    g = gen(8)
+    sizes = [20000003, 1, 16385, 70000, 9, 40000001, 8191, 500001, 3000000, 17, 1000003, 16384] + [5000 + 977 * i for i in range(60)]
+    types = [F32, BF, HF]
+    tensors = [randn(g, n, dtype=types[i % 3], scale=10.0 ** -(i % 3)) for i, n in enumerate(sizes)]
+    kinds = [HF, F32, BF]
+    check(moe, tensors, max_norm, out=[torch.full_like(t, 7.0, dtype=kinds[i // 3 % 3] if t.dtype == F32 else t.dtype)
+                                       for i, t in enumerate(tensors)] if out else None)

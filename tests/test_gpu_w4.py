@@ -266,3 +266,32 @@ def test_codes_past_32_bits(moe):
     w = moe.W4Weights(buf[:, :K // 2], torch.randint(118, 124, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8))
     for M in (1, 20):
         check(moe, randn(g, M, K, dtype=BF), w, *weights64(w), F32)
+
+
+# one and two rows, tiles, rows held in registers, rows shared through LDS
+EACH_KERNEL = [(1, 70, 1024), (2, 300, 1056), (4, 70, 160), (30, 530, 160), (3, 16390, 160), (20, 32769, 160), (40, 20485, 160)]
+
+
+@pytest.mark.parametrize("dt", [BF, HF], ids=["bf16", "f16"])
+@pytest.mark.parametrize("M,N,K", EACH_KERNEL)
+def test_scales_at_their_ends_in_each_kernel(moe, M, N, K, dt):
+    """UE8M0 bytes 2 and 252, alone and beside others.  252: |x| below 2^-10 keeps a sum of 1056
+    terms up to 6 * 2^125 in fp32's range."""
+    g = gen(M + N)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    x = randn(g, M, K, dtype=dt)
+    for lo, hi in ((2, 3), (200, 245), (2, 100)):
+        w = moe.W4Weights(codes, torch.randint(lo, hi, (N, K // 32), generator=g, device="cuda", dtype=torch.uint8))
+        check(moe, x, w, *weights64(w), F32)
+    w = moe.W4Weights(codes, torch.full((N, K // 32), 252, dtype=torch.uint8, device="cuda"))
+    check(moe, (x.float() * 2.0 ** -13).to(dt), w, *weights64(w), F32)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("M,N,K", EACH_KERNEL)
+def test_fp16_below_its_normal_numbers(moe, M, N, K, kind):
+    """x of subnormal fp16 alone: its products with the codes are exact in fp32 all the same."""
+    g = gen(M + N + 1)
+    x = (randn(g, M, K) * 2.0 ** -18).to(HF)
+    w, w64, mag = weights(moe, g, N, K, kind, zeros=kind[0] == "int4")
+    check(moe, x, w, w64, mag, F32)
