@@ -588,3 +588,40 @@ def test_gradients_of_saturated_sigmoids(moe, E):
     got = moe.moe_fp4_router_loss_backward(logits, idx, r, dbalance=dbal, score=moe.SCORE_SIGMOID)
     want, e, _ = backward64(logits, idx, r, dbal, None, None, None, True, None, None)
     bounded(got, want, e, F32, "dlogits")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,starts", [(1000, 384, [7, 7, 300, 301, 301, 990]), (6000, 40, [2500, 2500, 5990, 5999]),
+                                        (300, 700, [299, 300, 300]), (90, 20, [4 * i for i in range(11, 22)]), (4096, 130, [4096, 4096])])
+def test_forward_of_late_sequences(moe, T, E, starts, score):
+    """Tokens in front of the first sequence and behind the last one, which are in none."""
+    g = gen(T + E)
+    logits, idx, _, _, mask = batch(g, T, E, 2, 0, F32, True)
+    seqs = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    r = check_forward(moe, logits, idx, score == "sigmoid", seqs, mask)
+    assert int(r.tokens.sum()) == int(mask[starts[0]:starts[-1]].sum())
+
+
+@pytest.mark.parametrize("dt", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,S", [(60001, 40, 16, 1500), (40001, 384, 6, 700), (20001, 700, 16, 30)])
+def test_several_sequences_of_a_group_of_lanes(moe, T, E, k, S, score, dt):
+    """Batches that give a group of lanes several tokens, of several sequences, some of them empty or
+    masked: into new results, added to what is there, over the logits."""
+    sigmoid = score == "sigmoid"
+    g = gen(T + S)
+    logits, idx, gates, seqs, mask = batch(g, T, E, k, S, dt, True)
+    logits = logits.nan_to_num()
+    r = check_forward(moe, logits, idx, sigmoid, seqs, mask)
+    a, b, dg = randn(g, S), randn(g, S), randn(g, T, k)
+    kw = dict(dbalance=a, dz=b, gates=gates, dgates=dg, score=int(sigmoid), seqs=seqs, mask=mask)
+    got = moe.moe_fp4_router_loss_backward(logits, idx, r, **kw)
+    want, e, none = backward64(logits, idx, r, a, b, gates, dg, sigmoid, seqs, mask)
+    assert not bool(none.any())
+    bounded(got, want, e, dt, "dlogits")
+    base = randn(g, T, E)
+    acc = moe.moe_fp4_router_loss_backward(logits, idx, r, dlogits=base.clone(), accumulate=True, **kw)
+    bounded(acc, base.double() + want, e + U32 * (base.double() + want).abs(), F32, "+=")
+    assert torch.equal(acc[~mask], base[~mask])
+    moe.moe_fp4_router_loss_backward(logits, idx, r, dlogits=logits, **kw)
+    assert torch.equal(logits, got)

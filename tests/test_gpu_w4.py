@@ -295,3 +295,12 @@ def test_fp16_below_its_normal_numbers(moe, M, N, K, kind):
     x = (randn(g, M, K) * 2.0 ** -18).to(HF)
     w, w64, mag = weights(moe, g, N, K, kind, zeros=kind[0] == "int4")
     check(moe, x, w, w64, mag, F32)
+
+
+@pytest.mark.parametrize("kind", KINDS, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 40, 65536), (2, 33, 40000), (5, 40, 65536), (20, 50, 32800), (4, 16390, 15392), (18, 32770, 10240)])
+def test_long_sums(moe, M, N, K, kind):
+    """The most inputs, more than a workgroup's threads or chunks take at once."""
+    g = gen(M + N)
+    w, w64, mag = weights(moe, g, N, K, kind, zeros=kind[0] == "int4")
+    check(moe, randn(g, M, K, dtype=BF), w, w64, mag, F32)
