@@ -15,9 +15,16 @@
 // 76 us, 34 now; with 16 lanes 51, for its registers).  A lane keeps the same columns for every token: the sums
 // over tokens stay in registers, and so do the coefficients c of the backward pass.
 //
+// Sums over tokens are held in fp32, the products' sum and that of the pieces' lse^2 in fp64.  An fp32
+// sum's additions are a tree (a lane's T L / 2^17 tokens, 64 / L groups, eight waves, 16 rows of
+// pieces, 16 of those), so that errors grow slowly: of 16384 tokens and of 2^20 alike, 384
+// experts, probs are off by 3.9 * 2^-24 at most and 0.9 on average, balance by 1, z by 2.  N sums of
+// 64 bits in a lane would cost waves.
+//
 // One MI355X: forward, 16384 tokens of 384 experts in fp32, 25 MB, 11.2 us and 8.9 for the
-// columns (both chains of loads that wait for one another: offsets, rows, pieces); 64 tokens
-// 5.5 us.  Backward 14.1 us (50 MB, 3.6 TB/s); 65536 tokens, sigmoid, bf16, 34 us for 101 MB, of which
+// columns (both chains of loads that wait for one another: offsets, rows, pieces), with sigmoids
+// the same, bf16 0.5-1.5 less; 64 sequences in place of 8 53 in all, for a workgroup takes its pieces one
+// after the other; 64 tokens 5.5 us.  Backward 14.1 us (50 MB, 3.6 TB/s); 65536 tokens, sigmoid, bf16, 34 us for 101 MB, of which
 // the vector units are busy 59 %: about 25 instructions an element.
 #include "block_device.h"
 #include "router_loss.h"
@@ -447,9 +454,12 @@ __global__ void __launch_bounds__(32 * kColumnRows) router_loss_columns_kernel(R
 }
 
 constexpr int kBackWaves = 4;  // of a workgroup
-// Waves that a SIMD holds by the registers that they take, and so many a launch has.  (Of 65536
+// Waves of a launch for each SIMD: as many as it holds of them at 384 experts.  (Of 65536
 // tokens' bf16 logits with sigmoids, at 128 registers and four waves 34 us; 47 with one
 // register more, and 43 where the compiler is told to keep to four, for the order it then takes.)
+// Elsewhere the registers may hold one wave fewer, and some workgroups then start late: sigmoids of 513
+// to 768 experts in 16 bits with results in them (130 registers), and sigmoids of fp32 logits from
+// 385 to 512 and from 769 experts on (169 to 175).
 template <typename T, int N, bool Sigmoid>
 constexpr int kBackOfSimd = !Sigmoid || (T::kType != kF32 && N <= 12) ? 4 : 3;
 

@@ -241,7 +241,9 @@ void launch_type(const W4Args& a, hipStream_t stream) {
 //     whose workgroups are 256 there; 16384 x 5120: 19.0 held; 65536 x 5120: 74, 54
 //   shared through LDS (tiles, shared): 8 rows, int4 groups of 64, 32768 x 5120: 38, 47; 65536 x
 //     5120: 75, 54; 32 rows, MX, 24576 x 5120: 40, 45; 65536 x 5120: 101, 56; 64 rows, 16384 x 5120:
-//     34, 50; 24576 x 5120: 61, 52; 65536 x 5120: 127, 63
+//     34, 50; 24576 x 5120: 61, 52; 65536 x 5120: 127, 60
+// All of these are at K = 5120 or near it, most with MX and bf16: at other K the crossings may lie
+// elsewhere, since a workgroup's work grows with K.
 hipError_t launch_w4(const W4Args& a, hipStream_t stream) {
   const bool hold = a.code == kMx || a.group >= 128;
   const int wide = a.M > 32 ? 20480 : a.M > 16 ? 32768 : 49152;  // columns from which rows are shared

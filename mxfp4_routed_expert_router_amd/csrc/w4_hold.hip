@@ -219,7 +219,8 @@ void launch_group(const W4Args& a, hipStream_t stream) {
   const int tiles = (a.N + 15) / 16, blocks = tiles < kHoldBlocks ? tiles : kHoldBlocks;
   const dim3 grid(blocks, (a.M + 15) / 16);
   const int units = (a.K + 127) / 128;
-  // chunks of at most 40 units, alike long
+  // chunks of at most 40 units, alike long; a wave's four units run as five, one of zeros (16 rows of
+  // 16384 x 4096 17.4 us, x 5120 19.0)
   const int chunks = (units + 39) / 40, per = (units + chunks - 1) / chunks, uw = (per + kHoldWaves - 1) / kHoldWaves;
   int shift = 5;  // of inputs to scales
   while (1 << shift < a.group) ++shift;

@@ -9,7 +9,9 @@
 //
 // One row of 9216 x 5120, MX: 8.0 us for 25.2 MB; of 65536 x 5120 33.8 us (5.3 TB/s), bound by the
 // bytes; of 288 x 5120 2.8 us, a launch and one load's latency.  int4 takes half as long
-// again (51 us at 65536 x 5120): three instructions more for four codes.
+// again (50 us at 65536 x 5120) with 1.44 times the vector instructions, which keep their units 49 %
+// busy (MX 52 %): neither they nor the bytes (3.4 TB/s) bound it; a workgroup's waves wait for their
+// loads, of half as many columns at a time.
 #include "w4_device.h"
 
 namespace moe_fp4 {
